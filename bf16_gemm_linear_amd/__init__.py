@@ -29,6 +29,9 @@ __all__ = [
     "quant_int8", "quant_int8_rows", "OP_PALETTE_ANALYZE", "OP_PALETTE_GEMM", "PaletteWeight",
     "palette_encode", "palette_decode", "palette_gemm",
     "prune_compress", "decompress", "quant_fp8", "gemm", "dense_gemm", "workspace_size", "plan",
+    "quant_mxfp4", "dequant_mxfp4", "gemm_mxfp4", "gated_mxfp4", "rmsnorm", "ffn_mxfp4", "mxfp4_workspace_size",
+    "mxfp4_scale_index", "NORM_BF16", "NORM_FP8_ROWS", "NORM_INT8_ROWS", "NORM_FP8_GROUPS", "NORM_MXFP4",
+    "MXFP4_GEMM", "MXFP4_FFN",
     "probe_mfma_layout", "probe_mfma_rate", "probe_copy", "probe_read", "probe_ring",
 ]
 
@@ -37,6 +40,8 @@ SCALE_DYNAMIC, SCALE_STATIC = 0, 1
 OP_GEMM, OP_QUANT, OP_DENSE_GEMM, OP_GEMM_QX, OP_PALETTE_ANALYZE, OP_PALETTE_GEMM = 0, 1, 2, 3, 4, 5
 OP_GEMM_ROWS_QX = 6
 OP_GEMM_GROUPS = 7
+NORM_BF16, NORM_FP8_ROWS, NORM_INT8_ROWS, NORM_FP8_GROUPS, NORM_MXFP4 = 0, 1, 2, 3, 4
+MXFP4_GEMM, MXFP4_FFN = 0, 1
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 lib_path = os.path.join(_HERE, "libsp24.so")
@@ -91,6 +96,13 @@ _SIGS = {
     "sp24_palette_decode": [ctypes.POINTER(_PaletteStruct), _i64, _i64, _vp, _vp],
     "sp24_palette_gemm": [_i64, _i64, _i64, _vp, ctypes.POINTER(_PaletteStruct), _vp, _vp, _sz, _vp],
     "sp24_plan_gemm": [_int, _int, _i64, _i64, _i64, ctypes.POINTER(Plan)],
+    "sp24_quant_mxfp4": [_vp, _i64, _i64, _vp, _vp, _vp],
+    "sp24_dequant_mxfp4": [_vp, _vp, _i64, _i64, _vp, _vp],
+    "sp24_gemm_mxfp4": [_i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
+    "sp24_gated_mxfp4": [_i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp],
+    "sp24_rmsnorm": [_int, _i64, _i64, _i64, _vp, _vp, _vp, _vp, ctypes.c_float, _vp, _vp, _vp],
+    "sp24_ffn_mxfp4": [_i64, _i64, _i64, _vp, _vp, _vp, _vp, ctypes.c_float, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
+    "sp24_mxfp4_workspace_size": [_int, _i64, _i64, _i64],
     "sp24_status_string": [_int],
     "sp24_version": [],
     "sp24_probe_mfma_layout": [_int, _vp, _vp, _vp, _vp, _int, _vp],
@@ -109,6 +121,7 @@ for _name, _args in _SIGS.items():
     _f.argtypes = _args
     _f.restype = _int
 lib.sp24_workspace_size.restype = _sz
+lib.sp24_mxfp4_workspace_size.restype = _sz
 lib.sp24_status_string.restype = ctypes.c_char_p
 
 
@@ -738,6 +751,186 @@ def dense_gemm(x, w, x_scale=None, w_scale=None, out=None, ws=None):
 
 
 # --------------------------------------------------------------------------- probes
+
+_U8, _BF16, _F32 = torch.uint8, torch.bfloat16, torch.float32
+
+
+def mxfp4_workspace_size(op: int, m: int, n: int, k: int) -> int:
+    """Workspace bytes of an MXFP4 call (MXFP4_GEMM: m, n, k; MXFP4_FFN: m, f, d)."""
+    return int(lib.sp24_mxfp4_workspace_size(op, m, n, k))
+
+
+def mxfp4_scale_index(rows: int, cols: int, device=None) -> torch.Tensor:
+    """Where the scale byte of block b of row r is stored: int64 [rows, cols/32].  Scales in row-major
+    order go into storage order with `stored[index] = scales`, and back with `scales = stored[index]`
+    (a load-time helper; the kernels read storage order)."""
+    if rows < 1 or cols < 128 or cols % 128:
+        raise ValueError("MXFP4 operands have rows >= 1 and a multiple of 128 columns")
+    b = torch.arange(cols // 32, device=device)
+    w, words = b // 4, cols // 128
+    width = torch.clamp(words - 4 * (w // 4), max=4)
+    r = torch.arange(rows, device=device)[:, None]
+    return 4 * (4 * rows * (w // 4) + r * width + w % 4) + b % 4
+
+
+def _mx4_operand(codes, scales, name, device=None):
+    """(rows, cols) of an MXFP4 operand: codes uint8 [rows, cols/2], scales uint8 of rows * cols/32."""
+    _need(codes, name + " codes", _U8, 2, device)
+    _need(scales, name + " scales", _U8, 1, codes.device)
+    rows, cols = codes.shape[0], 2 * codes.shape[1]
+    if cols % 128 or scales.numel() * 32 != rows * cols:
+        raise ValueError("%s: codes [%d, %d] need a multiple of 64 columns and %d scales, got %d"
+                         % (name, rows, cols // 2, rows * cols // 32, scales.numel()))
+    return rows, cols
+
+
+def _mx4_out(out, name, dtype, shape, device):
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _need(out, name, dtype, len(shape), device)
+    if out.shape != shape:
+        raise ValueError("%s must be %s" % (name, list(shape)))
+    return out
+
+
+def quant_mxfp4(x: torch.Tensor, out: torch.Tensor | None = None, scales: torch.Tensor | None = None):
+    """bf16 [rows, cols] (cols % 128 == 0) -> MXFP4 (codes uint8 [rows, cols/2], scales uint8
+    [rows * cols/32] in storage order, see mxfp4_scale_index)."""
+    _need(x, "x", _BF16, 2)
+    rows, cols = x.shape
+    if cols % 128:
+        raise ValueError("MXFP4 needs a multiple of 128 columns, got %d" % cols)
+    dev = x.device
+    out = _mx4_out(out, "out", _U8, (rows, cols // 2), dev)
+    scales = _mx4_out(scales, "scales", _U8, (rows * cols // 32,), dev)
+    _check("sp24_quant_mxfp4", lib.sp24_quant_mxfp4(x.data_ptr(), rows, cols, out.data_ptr(), scales.data_ptr(),
+                                                    _stream(dev)))
+    return out, scales
+
+
+def dequant_mxfp4(codes: torch.Tensor, scales: torch.Tensor, out: torch.Tensor | None = None):
+    """The bf16 values [rows, cols] that MXFP4 codes and scales stand for (exact)."""
+    rows, cols = _mx4_operand(codes, scales, "operand")
+    dev = codes.device
+    out = _mx4_out(out, "out", _BF16, (rows, cols), dev)
+    _check("sp24_dequant_mxfp4", lib.sp24_dequant_mxfp4(codes.data_ptr(), scales.data_ptr(), rows, cols,
+                                                        out.data_ptr(), _stream(dev)))
+    return out
+
+
+def gemm_mxfp4(x_codes, x_scales, w_codes, w_scales, out=None, ws=None):
+    """Y = X . W^T of MXFP4 operands X [m, k] and W [n, k] (codes and scales of each); bf16 [m, n]."""
+    m, k = _mx4_operand(x_codes, x_scales, "x")
+    dev = x_codes.device
+    n, kw = _mx4_operand(w_codes, w_scales, "w", dev)
+    if kw != k:
+        raise ValueError("w has %d columns, x has %d" % (kw, k))
+    out = _mx4_out(out, "out", _BF16, (m, n), dev)
+    nbytes = lib.sp24_mxfp4_workspace_size(MXFP4_GEMM, m, n, k)
+    ws = _workspace(nbytes, dev, ws)
+    _check("sp24_gemm_mxfp4", lib.sp24_gemm_mxfp4(m, n, k, x_codes.data_ptr(), x_scales.data_ptr(),
+                                                  w_codes.data_ptr(), w_scales.data_ptr(), out.data_ptr(),
+                                                  None if ws is None else ws.data_ptr(), nbytes, _stream(dev)))
+    return out
+
+
+def gated_mxfp4(x_codes, x_scales, w_codes, w_scales, quantise=False, out=None, out_scales=None):
+    """silu(X Wg^T) * (X Wu^T) of MXFP4 operands, W = [f gate rows; f up rows]: bf16 [m, f], or with
+    quantise=True (f % 128 == 0) MXFP4 (codes, scales), the X of the next gemm_mxfp4."""
+    m, k = _mx4_operand(x_codes, x_scales, "x")
+    dev = x_codes.device
+    n, kw = _mx4_operand(w_codes, w_scales, "w", dev)
+    if kw != k or n % 2:
+        raise ValueError("w must be [2 f, %d] values, got [%d, %d]" % (k, n, kw))
+    f = n // 2
+    if quantise:
+        if f % 128:
+            raise ValueError("an MXFP4 output needs a multiple of 128 columns, got %d" % f)
+        out = _mx4_out(out, "out", _U8, (m, f // 2), dev)
+        out_scales = _mx4_out(out_scales, "out_scales", _U8, (m * f // 32,), dev)
+    else:
+        if out_scales is not None:
+            raise ValueError("out_scales goes with quantise=True")
+        out = _mx4_out(out, "out", _BF16, (m, f), dev)
+    _check("sp24_gated_mxfp4", lib.sp24_gated_mxfp4(
+        m, f, k, x_codes.data_ptr(), x_scales.data_ptr(), w_codes.data_ptr(), w_scales.data_ptr(),
+        None if quantise else out.data_ptr(), out.data_ptr() if quantise else None,
+        out_scales.data_ptr() if quantise else None, _stream(dev)))
+    return (out, out_scales) if quantise else out
+
+
+def _norm_inputs(x, weight, residual, residual_out):
+    _need(x, "x", _BF16, 2)
+    m, k = x.shape
+    _need(weight, "weight", _BF16, 1, x.device)
+    if weight.numel() != k:
+        raise ValueError("weight must hold %d values" % k)
+    if residual is not None:
+        _need(residual, "residual", _BF16, 2, x.device)
+        if residual.shape != x.shape:
+            raise ValueError("residual must be [%d, %d]" % (m, k))
+        residual_out = _mx4_out(residual_out, "residual_out", _BF16, (m, k), x.device)
+    elif residual_out is not None:
+        raise ValueError("residual_out goes with a residual")
+    return m, k, residual_out
+
+
+def rmsnorm(x, weight, kind=NORM_BF16, residual=None, eps=1e-6, group=128, out=None, scales=None, residual_out=None):
+    """RMS norm of the rows of x (+ residual) in the form the next product reads: (out, scales,
+    residual_out), scales None for NORM_BF16 and residual_out (bf16 of x + residual; may be `residual`
+    itself) None without a residual.
+
+    NORM_BF16 bf16 [m, k]; NORM_FP8_ROWS / NORM_INT8_ROWS codes [m, k] (uint8 or float8_e4m3fn / int8)
+    and scales fp32 [m]; NORM_FP8_GROUPS scales fp32 [m, k/group]; NORM_MXFP4 codes uint8 [m, k/2] and
+    scales uint8 [m * k/32] in storage order."""
+    m, k, residual_out = _norm_inputs(x, weight, residual, residual_out)
+    dev = x.device
+    if kind == NORM_MXFP4:
+        if k % 128:
+            raise ValueError("MXFP4 needs a multiple of 128 columns, got %d" % k)
+        out = _mx4_out(out, "out", _U8, (m, k // 2), dev)
+        scales = _mx4_out(scales, "scales", _U8, (m * k // 32,), dev)
+    elif kind == NORM_BF16:
+        if scales is not None:
+            raise ValueError("a bf16 output has no scales")
+        out = _mx4_out(out, "out", _BF16, (m, k), dev)
+    elif kind in (NORM_FP8_ROWS, NORM_INT8_ROWS, NORM_FP8_GROUPS):
+        if kind == NORM_FP8_GROUPS and (group < 8 or group % 8 or k % group):
+            raise ValueError("group must be a multiple of 8 that divides k=%d" % k)
+        dt = torch.int8 if kind == NORM_INT8_ROWS else _CODE_T
+        out = _mx4_out(out, "out", dt, (m, k), dev) if out is not None else torch.empty(
+            (m, k), dtype=torch.int8 if kind == NORM_INT8_ROWS else _U8, device=dev)
+        scales = _mx4_out(scales, "scales", _F32, (m, k // group) if kind == NORM_FP8_GROUPS else (m,), dev)
+    _check("sp24_rmsnorm", lib.sp24_rmsnorm(
+        kind, m, k, group, x.data_ptr(), None if residual is None else residual.data_ptr(),
+        None if residual is None else residual_out.data_ptr(), weight.data_ptr(), eps,
+        None if out is None else out.data_ptr(), None if scales is None else scales.data_ptr(), _stream(dev)))
+    return out, scales, residual_out
+
+
+def ffn_mxfp4(x, weight, gu_codes, gu_scales, down_codes, down_scales, residual=None, eps=1e-6, out=None,
+              residual_out=None, ws=None):
+    """A pre-norm feed-forward block in MXFP4: y = down(silu(gate(v)) * up(v)), v the RMS norm of
+    x (+ residual) under `weight`; gate_up W [2 f, d] (gate rows first) and down W [d, f] as MXFP4
+    codes and scales.  Returns (y bf16 [m, d], residual_out or None); bit for bit rmsnorm(NORM_MXFP4),
+    gated_mxfp4(quantise=True) and gemm_mxfp4 in turn."""
+    m, d, residual_out = _norm_inputs(x, weight, residual, residual_out)
+    dev = x.device
+    n2, kd = _mx4_operand(gu_codes, gu_scales, "gate_up", dev)
+    nd, f = _mx4_operand(down_codes, down_scales, "down", dev)
+    if kd != d or nd != d or n2 != 2 * f:
+        raise ValueError("gate_up must be [%d, %d] values and down [%d, %d], got [%d, %d] and [%d, %d]"
+                         % (2 * f, d, d, f, n2, kd, nd, f))
+    out = _mx4_out(out, "out", _BF16, (m, d), dev)
+    nbytes = lib.sp24_mxfp4_workspace_size(MXFP4_FFN, m, f, d)
+    ws = _workspace(nbytes, dev, ws)
+    _check("sp24_ffn_mxfp4", lib.sp24_ffn_mxfp4(
+        m, d, f, x.data_ptr(), None if residual is None else residual.data_ptr(),
+        None if residual is None else residual_out.data_ptr(), weight.data_ptr(), eps, gu_codes.data_ptr(),
+        gu_scales.data_ptr(), down_codes.data_ptr(), down_scales.data_ptr(), out.data_ptr(),
+        None if ws is None else ws.data_ptr(), nbytes, _stream(dev)))
+    return out, residual_out
+
 
 def probe_mfma_layout(variant: int, a: torch.Tensor, b: torch.Tensor, idx: torch.Tensor,
                       c: torch.Tensor, n_exp: int):

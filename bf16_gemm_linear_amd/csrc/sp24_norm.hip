@@ -1,0 +1,233 @@
+// RMS norm with the residual's addition, its output in bf16, in 8 bits with scales or in
+// MXFP4: per row, t = x + residual (fp32, unrounded; bf16_rne(t) is the new residual),
+// v = t rstd w with rstd = 1 / sqrt(mean(t^2) + eps).
+//
+// Memory-bound: 2 bytes read a value (6 moved with a residual) and 1 written (E4M3, INT8).
+// One pass: a row stays in registers as fp32 from the loads to the codes, T threads a row
+// with NV vectors of 8 values each.  The codes do not wait for rstd: with u = t w, a scale
+// is s = max|u| rstd / top, so v / s = u (top / max|u|), and one reduction over the row
+// gives sum t^2 and max|u| together (for groups, the maxima are taken by shuffles at the
+// same time).  Sums are fp32 in a fixed order.
+#include "sp24_fp8.hpp"
+#include "sp24_mx4.hpp"
+
+namespace sp24 {
+namespace {
+
+// The codes' divisor for values u with largest magnitude amax and scale a / top, a = amax
+// rstd: u (top / amax), the factor kept as hi + lo so that the quotient carries one
+// rounding; maxima below 2^-60 are scaled up by 2^80 first (exact), so that the factor
+// stays finite.  a = 0: scale 1, codes 0.  a Inf or NaN: scale NaN, codes 0.
+struct NormDiv {
+  float hi, lo, up;
+  bool on;
+};
+
+template <int KIND>
+__device__ __forceinline__ float norm_scale(uint32_t key, float rstd, NormDiv& d) {
+  constexpr float top = KIND == SP24_NORM_INT8_ROWS ? 127.0f : 448.0f;
+  const float amax = __uint_as_float(key), a = amax * rstd;
+  d.on = a > 0.0f && a < __builtin_inff();
+  d.up = amax < 0x1p-60f ? 0x1p80f : 1.0f;
+  const float b = amax * d.up;
+  d.hi = top / b;
+  d.lo = __builtin_fmaf(-d.hi, b, top) / b;
+  return a == 0.0f ? 1.0f : d.on ? a / top : __uint_as_float(0x7FC00000u);
+}
+
+template <int KIND>
+__device__ __forceinline__ u32x2 norm_codes8(const float* u, const NormDiv& d) {
+  float q[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float t = u[e] * d.up;
+    q[e] = d.on ? __builtin_fmaf(t, d.hi, t * d.lo) : 0.0f;
+  }
+  if constexpr (KIND == SP24_NORM_INT8_ROWS) {
+    return u32x2{f32_to_i8(q[0]) | (f32_to_i8(q[1]) << 8) | (f32_to_i8(q[2]) << 16) | (f32_to_i8(q[3]) << 24),
+                 f32_to_i8(q[4]) | (f32_to_i8(q[5]) << 8) | (f32_to_i8(q[6]) << 16) | (f32_to_i8(q[7]) << 24)};
+  } else {
+    return u32x2{f32x2_to_e4m3(q[0], q[1]) | (f32x2_to_e4m3(q[2], q[3]) << 16),
+                 f32x2_to_e4m3(q[4], q[5]) | (f32x2_to_e4m3(q[6], q[7]) << 16)};
+  }
+}
+
+// T threads a row (64: one wave, four rows a workgroup), NV vectors of 8 values a thread.
+// Groups (SP24_NORM_FP8_GROUPS): segments of `seg` lanes, seg a power of two dividing the
+// group's vectors; where a group is more than one segment its maximum is collected in LDS
+// (integer maxima: the order does not matter).
+template <int KIND, int T, int NV>
+__global__ __launch_bounds__(T < 256 ? 256 : T) void rmsnorm_kernel(
+    const uint16_t* __restrict__ x, const uint16_t* residual, uint16_t* residual_out,
+    const uint16_t* __restrict__ w, int64_t m, int k, float eps, int group, int seg, void* __restrict__ out,
+    void* __restrict__ scales) {
+  constexpr int RPB = T < 256 ? 256 / T : 1, NW = T / 64;
+  constexpr bool GROUPS = KIND == SP24_NORM_FP8_GROUPS;
+  __shared__ float sh_sum[RPB * NW];
+  __shared__ uint32_t sh_max[RPB * NW];
+  extern __shared__ uint32_t gmax[];  // [RPB][groups], only where a group is more than a segment
+
+  const int tl = threadIdx.x % T, rl = threadIdx.x / T, lane = threadIdx.x & 63;
+  const int64_t row = (int64_t)blockIdx.x * RPB + rl;
+  const int nv = row < m ? k / 8 : 0;
+  const size_t base = (size_t)row * (k / 8);
+  const int vpg = GROUPS ? group / 8 : 1, ng = GROUPS ? k / group : 1;
+  const bool in_lds = GROUPS && vpg != seg;
+  if (in_lds) {
+    for (int i = threadIdx.x; i < RPB * ng; i += (T < 256 ? 256 : T)) gmax[i] = 0;
+    __syncthreads();
+  }
+
+  u32x4 xd[NV], rd[NV], wd[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int i = tl + j * T;
+    xd[j] = rd[j] = wd[j] = u32x4{0u, 0u, 0u, 0u};
+    if (i < nv) {
+      xd[j] = reinterpret_cast<const u32x4*>(x)[base + i];
+      if (residual != nullptr) rd[j] = reinterpret_cast<const u32x4*>(residual)[base + i];
+      wd[j] = reinterpret_cast<const u32x4*>(w)[i];
+    }
+  }
+  float u[NV][8], ss = 0.0f;
+  uint32_t key = 0, gkey[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int i = tl + j * T;
+    uint32_t mk = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t xe = (e & 1) ? xd[j][e / 2] & 0xFFFF0000u : xd[j][e / 2] << 16;
+      const uint32_t re = (e & 1) ? rd[j][e / 2] & 0xFFFF0000u : rd[j][e / 2] << 16;
+      float t = __uint_as_float(xe);
+      if (residual != nullptr) t += __uint_as_float(re);
+      ss = __builtin_fmaf(t, t, ss);
+      u[j][e] = t;
+    }
+    if (residual != nullptr && i < nv) {
+      reinterpret_cast<u32x4*>(residual_out)[base + i] =
+          u32x4{f32x2_to_bf16x2(u[j][0], u[j][1]), f32x2_to_bf16x2(u[j][2], u[j][3]),
+                f32x2_to_bf16x2(u[j][4], u[j][5]), f32x2_to_bf16x2(u[j][6], u[j][7])};
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t we = (e & 1) ? wd[j][e / 2] & 0xFFFF0000u : wd[j][e / 2] << 16;
+      // bf16 output keeps t (v = t rstd w, as the formula reads); the others u = t w
+      if constexpr (KIND != SP24_NORM_BF16) u[j][e] *= __uint_as_float(we);
+      mk = max(mk, __float_as_uint(u[j][e]) & 0x7FFFFFFFu);
+    }
+    key = max(key, mk);
+    if constexpr (GROUPS) {
+      for (int off = 1; off < seg; off <<= 1) mk = max(mk, (uint32_t)__shfl_xor((int)mk, off, 64));
+      gkey[j] = mk;
+      if (in_lds && i < nv && lane % seg == 0) atomicMax(&gmax[rl * ng + i / vpg], mk);
+    }
+  }
+
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) {
+    ss += __shfl_xor(ss, off, 64);
+    if constexpr (!GROUPS) key = max(key, (uint32_t)__shfl_xor((int)key, off, 64));
+  }
+  if constexpr (NW > 1) {
+    if (lane == 0) {
+      sh_sum[threadIdx.x / 64] = ss;
+      sh_max[threadIdx.x / 64] = key;
+    }
+    __syncthreads();
+    ss = 0.0f;
+    key = 0;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      ss += sh_sum[i];
+      key = max(key, sh_max[i]);
+    }
+  } else {
+    if (in_lds) __syncthreads();
+  }
+  const float rstd = 1.0f / __builtin_sqrtf(ss / (float)k + eps);
+
+  NormDiv d{0.0f, 0.0f, 1.0f, false};
+  if constexpr (KIND == SP24_NORM_FP8_ROWS || KIND == SP24_NORM_INT8_ROWS) {
+    const float s = norm_scale<KIND>(key, rstd, d);
+    if (tl == 0 && nv > 0) static_cast<float*>(scales)[row] = s;
+  }
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int i = tl + j * T;
+    if constexpr (KIND == SP24_NORM_BF16) {
+      if (i < nv) {
+        u32x4 o;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          o[e] = f32x2_to_bf16x2(u[j][2 * e] * rstd * __uint_as_float(wd[j][e] << 16),
+                                 u[j][2 * e + 1] * rstd * __uint_as_float(wd[j][e] & 0xFFFF0000u));
+        static_cast<u32x4*>(out)[base + i] = o;
+      }
+    } else if constexpr (KIND == SP24_NORM_MXFP4) {
+      uint32_t mk = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        u[j][e] *= rstd;
+        mk = max(mk, __float_as_uint(u[j][e]) & 0x7FFFFFFFu);
+      }
+      const uint32_t byte = mx4_block_byte<23>(mk);  // k % 128 == 0: the 16 lanes of a word are all in the row
+      const uint32_t word = mx4_word_of_blocks(byte, lane);
+      if (i < nv) {
+        static_cast<uint32_t*>(out)[base + i] = mx4_codes8(u[j], byte);
+        if ((lane & 15) == 0) static_cast<uint32_t*>(scales)[mx4_scale_word(row, i / 16, m, k)] = word;
+      }
+    } else {
+      if (i < nv) {
+        if constexpr (GROUPS) {
+          const int g = i / vpg;
+          const float s = norm_scale<KIND>(in_lds ? gmax[rl * ng + g] : gkey[j], rstd, d);
+          if (i % vpg == 0) static_cast<float*>(scales)[(size_t)row * ng + g] = s;
+        }
+        static_cast<u32x2*>(out)[base + i] = norm_codes8<KIND>(u[j], d);
+      }
+    }
+  }
+}
+
+template <int KIND, int T, int NV>
+hipError_t launch_norm_tn(const NormArgs& a, hipStream_t s) {
+  constexpr int RPB = T < 256 ? 256 / T : 1;
+  int seg = 1;
+  size_t lds = 0;
+  if (KIND == SP24_NORM_FP8_GROUPS) {
+    const int64_t vpg = a.group / 8;
+    while (seg < 64 && vpg % (2 * seg) == 0) seg *= 2;
+    if (vpg != seg) lds = (size_t)RPB * (a.k / a.group) * 4;
+  }
+  hipLaunchKernelGGL((rmsnorm_kernel<KIND, T, NV>), dim3((uint32_t)((a.m + RPB - 1) / RPB)),
+                     dim3(T < 256 ? 256 : T), lds, s, a.x, a.residual, a.residual_out, a.weight, a.m, (int)a.k,
+                     a.eps, (int)a.group, seg, a.out, a.scales);
+  return hipGetLastError();
+}
+
+// Threads a row by its length: a wave up to 2048 values, then one workgroup.
+template <int KIND>
+hipError_t launch_norm_kind(const NormArgs& a, hipStream_t s) {
+  const int64_t nv = a.k / 8;
+  if (nv <= 64) return launch_norm_tn<KIND, 64, 1>(a, s);
+  if (nv <= 256) return launch_norm_tn<KIND, 64, 4>(a, s);
+  if (nv <= 512) return launch_norm_tn<KIND, 256, 2>(a, s);
+  if (nv <= 1024) return launch_norm_tn<KIND, 256, 4>(a, s);
+  if (nv <= 2048) return launch_norm_tn<KIND, 512, 4>(a, s);
+  return launch_norm_tn<KIND, 1024, 8>(a, s);
+}
+
+}  // namespace
+
+hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t s) {
+  switch (a.kind) {
+    case SP24_NORM_BF16: return launch_norm_kind<SP24_NORM_BF16>(a, s);
+    case SP24_NORM_FP8_ROWS: return launch_norm_kind<SP24_NORM_FP8_ROWS>(a, s);
+    case SP24_NORM_INT8_ROWS: return launch_norm_kind<SP24_NORM_INT8_ROWS>(a, s);
+    case SP24_NORM_FP8_GROUPS: return launch_norm_kind<SP24_NORM_FP8_GROUPS>(a, s);
+    default: return launch_norm_kind<SP24_NORM_MXFP4>(a, s);
+  }
+}
+
+}  // namespace sp24

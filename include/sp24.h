@@ -452,6 +452,116 @@ int sp24_palette_decode(const sp24_palette_weight* pw, int64_t n, int64_t k, voi
 int sp24_palette_gemm(int64_t m, int64_t n, int64_t k, const void* x_bf16, const sp24_palette_weight* pw,
                       void* y_bf16, void* ws, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * MXFP4: microscaled 4-bit floating point (the OCP microscaling format), dense.
+ * A block of 32 consecutive values of a row shares one power-of-two scale; a
+ * value is e2m1 * 2^(scale byte - 127).
+ *   codes  [rows, cols/2] bytes: E2M1 codes (sign, 2 exponent bits, 1 mantissa
+ *          bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6), value 2i of a row in the low half of
+ *          its byte i;
+ *   scales rows * cols/32 bytes: E8M0 (2^(byte - 127), 255 = NaN), four blocks to
+ *          a 32-bit word (block 4w + j in byte j of word w), the cols/128 words of
+ *          a row in the storage order of the 2:4 metadata words: blocks of 4 words
+ *          (512 values), block after block, in each every row's words row after
+ *          row: word w of row r sits at 4*rows*(w/4) + r*min(4, cols/128 - 4*(w/4))
+ *          + w%4.  A K step of a row range is then contiguous.
+ * Rows are the tokens of an activation or the output channels of a weight;
+ * cols % 128 == 0 everywhere.  Rounding: the scale's exponent is floor(log2 amax)
+ * - 2 held to [-127, 127] (0 for a block of zeros), the code e2m1_rne(clamp(x /
+ * scale, -6, 6)).  A block with an Inf or a NaN gets scale byte 255 and codes 0:
+ * every product with it is NaN.
+ * ------------------------------------------------------------------------- */
+
+/* bf16 [rows, cols] -> MXFP4 codes and scales (bit-exact, see above).
+ *   rows >= 1, cols >= 128, cols % 128 == 0, rows * cols/128 < 2^31.  No
+ *   workspace, no host synchronisation. */
+int sp24_quant_mxfp4(const void* x_bf16, int64_t rows, int64_t cols, uint8_t* codes_out, uint8_t* scales_out,
+                     void* stream);
+
+/* The values that codes and scales stand for, in bf16 (exact: E2M1 times a power
+ * of two; overflow beyond bf16, which sp24_quant_mxfp4 never writes, gives Inf).
+ * Limits as sp24_quant_mxfp4. */
+int sp24_dequant_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, void* out_bf16,
+                       void* stream);
+
+/* Y = X . W^T of two MXFP4 operands; fp32 accumulation, bf16 output.
+ *   x_codes [m, k/2], x_scales m*k/32 bytes; w_codes [n, k/2], w_scales n*k/32
+ *   bytes; y_bf16 [m, n].
+ * Requires m, n >= 1, at most 2^21; k >= 128, k % 128 == 0, at most 2^30.  The sum over k is formed in a fixed order for a given (m, n, k): results
+ * are bitwise reproducible.  ws/ws_bytes: sp24_mxfp4_workspace_size(
+ * SP24_MXFP4_GEMM, m, n, k). */
+int sp24_gemm_mxfp4(int64_t m, int64_t n, int64_t k, const uint8_t* x_codes, const uint8_t* x_scales,
+                    const uint8_t* w_codes, const uint8_t* w_scales, void* y_bf16, void* ws, size_t ws_bytes,
+                    void* stream);
+
+/* The gated projection of a feed-forward block in one kernel:
+ *   h = silu(X Wg^T) * (X Wu^T),  silu(g) = g / (1 + exp(-g)),
+ * both products, the activation and their product in fp32, rounded once.
+ *   w_codes [2f, k/2]: the f gate rows, then the f up rows; w_scales 2f*k/32 bytes
+ *   (the storage order of one weight of 2f rows).
+ *   h_bf16 [m, f], or, with h_bf16 NULL, h in MXFP4: h_codes [m, f/2], h_scales
+ *   m*f/32 bytes (f % 128 == 0; blocks as sp24_quant_mxfp4 rounds them, from the
+ *   fp32 h).  Exactly one of the two outputs (SP24_ERR_MODE otherwise).
+ * Requires m, f >= 1, k >= 128, k % 128 == 0, k at most 2^30, m and 2f at most
+ * 2^21.  No workspace. */
+int sp24_gated_mxfp4(int64_t m, int64_t f, int64_t k, const uint8_t* x_codes, const uint8_t* x_scales,
+                     const uint8_t* w_codes, const uint8_t* w_scales, void* h_bf16, uint8_t* h_codes,
+                     uint8_t* h_scales, void* stream);
+
+/* Output forms of sp24_rmsnorm. */
+typedef enum sp24_norm_kind {
+  SP24_NORM_BF16 = 0,       /* out bf16 [m, k]; no scales */
+  SP24_NORM_FP8_ROWS = 1,   /* out E4M3 [m, k], scales fp32 [m]: sp24_gemm_rows's X */
+  SP24_NORM_INT8_ROWS = 2,  /* out int8 [m, k], scales fp32 [m]: sp24_gemm_rows's X */
+  SP24_NORM_FP8_GROUPS = 3, /* out E4M3 [m, k], scales fp32 [m, k/group]: sp24_gemm_groups's X */
+  SP24_NORM_MXFP4 = 4       /* out codes [m, k/2], scales m*k/32 bytes: sp24_gemm_mxfp4's X */
+} sp24_norm_kind;
+
+/* Root-mean-square norm of the rows of X + residual, in the form that the next
+ * product reads:
+ *   t = x + residual (residual NULL: t = x),  residual_out = bf16_rne(t),
+ *   v = t * w / sqrt(mean(t^2) + eps),
+ *   SP24_NORM_BF16: out = bf16_rne(v);
+ *   E4M3 and INT8: s = amax|v| / 448 (127) over the row or group, 1 where that is
+ *     0, out = the code of v / s (nearest even); a row or group whose amax is not
+ *     finite gets s = NaN and codes 0;
+ *   SP24_NORM_MXFP4: the blocks of v as sp24_quant_mxfp4 rounds them.
+ * All of it in fp32 from the unrounded t; v is never rounded to bf16 in between,
+ * so codes can differ by a rounding from those of a norm and a quantiser in turn.
+ *   x_bf16 [m, k]; residual_bf16 [m, k] or NULL; residual_out_bf16 [m, k], given
+ *   exactly when residual is (it may be the same buffer: an update in place);
+ *   weight_bf16 [k]; eps > 0 and finite (SP24_ERR_MODE otherwise).
+ * Requires 1 <= m <= 2^21, 8 <= k <= 65536, k % 8 == 0 (SP24_NORM_MXFP4: k % 128 == 0);
+ * group (SP24_NORM_FP8_GROUPS only, else ignored): group % 8 == 0, k % group == 0.
+ * Finite inputs whose squares sum beyond fp32 (|t| above about 1e18) are outside
+ * its range. */
+int sp24_rmsnorm(int kind, int64_t m, int64_t k, int64_t group, const void* x_bf16, const void* residual_bf16,
+                 void* residual_out_bf16, const void* weight_bf16, float eps, void* out, void* scales_out,
+                 void* stream);
+
+/* A pre-norm feed-forward block in MXFP4, three launches (four where the last
+ * product splits k): X + residual normed into MXFP4 (sp24_rmsnorm), the gated
+ * projection with an MXFP4 output (sp24_gated_mxfp4), the down-projection
+ * (sp24_gemm_mxfp4); bit for bit those calls in turn.
+ *   x_bf16, residual_bf16 (or NULL), residual_out_bf16, weight_bf16 [d], eps as
+ *   sp24_rmsnorm; gu_codes [2f, d/2] and gu_scales as sp24_gated_mxfp4; down_codes
+ *   [d, f/2], down_scales d*f/32 bytes; y_bf16 [m, d] (the residual is not added).
+ * Requires d % 128 == 0, d <= 65536, f % 128 == 0 and the limits of the three
+ * calls.  ws/ws_bytes: sp24_mxfp4_workspace_size(SP24_MXFP4_FFN, m, f, d). */
+int sp24_ffn_mxfp4(int64_t m, int64_t d, int64_t f, const void* x_bf16, const void* residual_bf16,
+                   void* residual_out_bf16, const void* weight_bf16, float eps, const uint8_t* gu_codes,
+                   const uint8_t* gu_scales, const uint8_t* down_codes, const uint8_t* down_scales, void* y_bf16,
+                   void* ws, size_t ws_bytes, void* stream);
+
+typedef enum sp24_mxfp4_op {
+  SP24_MXFP4_GEMM = 0, /* sp24_gemm_mxfp4 (m, n, k) */
+  SP24_MXFP4_FFN = 1   /* sp24_ffn_mxfp4 (m, n = f, k = d) */
+} sp24_mxfp4_op;
+
+/* Workspace bytes of an MXFP4 call (0 if none; also 0 for invalid arguments,
+ * which the call itself then rejects).  Host-only. */
+size_t sp24_mxfp4_workspace_size(int op, int64_t m, int64_t n, int64_t k);
+
 /* Workspace bytes needed by an op at a shape (0 if none; also 0 for invalid
  * arguments, which the op itself then rejects). */
 size_t sp24_workspace_size(int op, int dtype, int64_t m, int64_t n, int64_t k);
