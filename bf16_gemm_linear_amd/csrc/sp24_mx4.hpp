@@ -127,5 +127,8 @@ struct Mx4Args {
 };
 size_t mx4_gemm_ws_bytes(int64_t m, int64_t n, int64_t k);  // split-K partial sums (not gated)
 hipError_t launch_mx4_gemm(const Mx4Args& a, hipStream_t s);
+// sp24_mx4_stream.hip, sp24_mx4_tiled.hip
+hipError_t launch_mx4_stream(int rb, int rows, const Mx4Args& a, hipStream_t s);
+hipError_t launch_mx4_tiled(int cfg, int split, const Mx4Args& a, hipStream_t s);
 
 }  // namespace sp24

@@ -10,7 +10,9 @@ namespace {
 constexpr int64_t kMaxRows = (int64_t)1 << 21;  // rows of an operand: one workgroup of up to 1024 threads each
 constexpr int64_t kMaxNormK = 65536;            // a row lives in one workgroup's registers
 
-bool mx4_cols(int64_t k) { return k >= 128 && k % 128 == 0 && k <= kMaxDim; }
+constexpr int64_t kMaxK = (int64_t)1 << 24;     // 32-bit offsets inside a tile of 256 rows
+
+bool mx4_cols(int64_t k) { return k >= 128 && k % 128 == 0 && k <= kMaxK; }
 bool mx4_rows(int64_t n) { return n >= 1 && n <= kMaxRows; }
 
 size_t code_bytes(int64_t rows, int64_t cols) { return (size_t)rows * (cols / 2); }

@@ -473,8 +473,8 @@ int sp24_palette_gemm(int64_t m, int64_t n, int64_t k, const void* x_bf16, const
  * ------------------------------------------------------------------------- */
 
 /* bf16 [rows, cols] -> MXFP4 codes and scales (bit-exact, see above).
- *   rows >= 1, cols >= 128, cols % 128 == 0, rows * cols/128 < 2^31.  No
- *   workspace, no host synchronisation. */
+ *   rows >= 1, 128 <= cols <= 2^24, cols % 128 == 0, rows * cols/128 < 2^31.
+ *   No workspace, no host synchronisation. */
 int sp24_quant_mxfp4(const void* x_bf16, int64_t rows, int64_t cols, uint8_t* codes_out, uint8_t* scales_out,
                      void* stream);
 
@@ -487,7 +487,7 @@ int sp24_dequant_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t rows
 /* Y = X . W^T of two MXFP4 operands; fp32 accumulation, bf16 output.
  *   x_codes [m, k/2], x_scales m*k/32 bytes; w_codes [n, k/2], w_scales n*k/32
  *   bytes; y_bf16 [m, n].
- * Requires m, n >= 1, at most 2^21; k >= 128, k % 128 == 0, at most 2^30.  The sum over k is formed in a fixed order for a given (m, n, k): results
+ * Requires m, n >= 1, at most 2^21; 128 <= k <= 2^24, k % 128 == 0.  The sum over k is formed in a fixed order for a given (m, n, k): results
  * are bitwise reproducible.  ws/ws_bytes: sp24_mxfp4_workspace_size(
  * SP24_MXFP4_GEMM, m, n, k). */
 int sp24_gemm_mxfp4(int64_t m, int64_t n, int64_t k, const uint8_t* x_codes, const uint8_t* x_scales,
@@ -502,8 +502,8 @@ int sp24_gemm_mxfp4(int64_t m, int64_t n, int64_t k, const uint8_t* x_codes, con
  *   h_bf16 [m, f], or, with h_bf16 NULL, h in MXFP4: h_codes [m, f/2], h_scales
  *   m*f/32 bytes (f % 128 == 0; blocks as sp24_quant_mxfp4 rounds them, from the
  *   fp32 h).  Exactly one of the two outputs (SP24_ERR_MODE otherwise).
- * Requires m, f >= 1, k >= 128, k % 128 == 0, k at most 2^30, m and 2f at most
- * 2^21.  No workspace. */
+ * Requires m, f >= 1, m and 2f at most 2^21, 128 <= k <= 2^24, k % 128 == 0.  No
+ * workspace. */
 int sp24_gated_mxfp4(int64_t m, int64_t f, int64_t k, const uint8_t* x_codes, const uint8_t* x_scales,
                      const uint8_t* w_codes, const uint8_t* w_scales, void* h_bf16, uint8_t* h_codes,
                      uint8_t* h_scales, void* stream);
