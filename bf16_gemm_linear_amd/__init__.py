@@ -29,9 +29,8 @@ __all__ = [
     "quant_int8", "quant_int8_rows", "OP_PALETTE_ANALYZE", "OP_PALETTE_GEMM", "PaletteWeight",
     "palette_encode", "palette_decode", "palette_gemm",
     "prune_compress", "decompress", "quant_fp8", "gemm", "dense_gemm", "workspace_size", "plan",
-    "quant_mxfp4", "dequant_mxfp4", "gemm_mxfp4", "gated_mxfp4", "rmsnorm", "ffn_mxfp4", "mxfp4_workspace_size",
+    "quant_mxfp4", "dequant_mxfp4", "gemm_mxfp4", "gated_mxfp4", "rmsnorm", "ffn_mxfp4", "ffn_mxfp4_workspace_size",
     "mxfp4_scale_index", "NORM_BF16", "NORM_FP8_ROWS", "NORM_INT8_ROWS", "NORM_FP8_GROUPS", "NORM_MXFP4",
-    "MXFP4_GEMM", "MXFP4_FFN",
     "probe_mfma_layout", "probe_mfma_rate", "probe_copy", "probe_read", "probe_ring",
 ]
 
@@ -41,7 +40,6 @@ OP_GEMM, OP_QUANT, OP_DENSE_GEMM, OP_GEMM_QX, OP_PALETTE_ANALYZE, OP_PALETTE_GEM
 OP_GEMM_ROWS_QX = 6
 OP_GEMM_GROUPS = 7
 NORM_BF16, NORM_FP8_ROWS, NORM_INT8_ROWS, NORM_FP8_GROUPS, NORM_MXFP4 = 0, 1, 2, 3, 4
-MXFP4_GEMM, MXFP4_FFN = 0, 1
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 lib_path = os.path.join(_HERE, "libsp24.so")
@@ -98,11 +96,11 @@ _SIGS = {
     "sp24_plan_gemm": [_int, _int, _i64, _i64, _i64, ctypes.POINTER(Plan)],
     "sp24_quant_mxfp4": [_vp, _i64, _i64, _vp, _vp, _vp],
     "sp24_dequant_mxfp4": [_vp, _vp, _i64, _i64, _vp, _vp],
-    "sp24_gemm_mxfp4": [_i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
+    "sp24_gemm_mxfp4": [_i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp],
     "sp24_gated_mxfp4": [_i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp],
     "sp24_rmsnorm": [_int, _i64, _i64, _i64, _vp, _vp, _vp, _vp, ctypes.c_float, _vp, _vp, _vp],
     "sp24_ffn_mxfp4": [_i64, _i64, _i64, _vp, _vp, _vp, _vp, ctypes.c_float, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
-    "sp24_mxfp4_workspace_size": [_int, _i64, _i64, _i64],
+    "sp24_ffn_mxfp4_workspace_size": [_i64, _i64, _i64],
     "sp24_status_string": [_int],
     "sp24_version": [],
     "sp24_probe_mfma_layout": [_int, _vp, _vp, _vp, _vp, _int, _vp],
@@ -121,7 +119,7 @@ for _name, _args in _SIGS.items():
     _f.argtypes = _args
     _f.restype = _int
 lib.sp24_workspace_size.restype = _sz
-lib.sp24_mxfp4_workspace_size.restype = _sz
+lib.sp24_ffn_mxfp4_workspace_size.restype = _sz
 lib.sp24_status_string.restype = ctypes.c_char_p
 
 
@@ -144,8 +142,12 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+# the current stream's handle without building a Stream object (2 us a call)
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _stream(dev):
-    return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+    return _raw_stream(dev.index)
 
 
 def _need(t, name, dtype=None, ndim=None, device=None):
@@ -755,9 +757,9 @@ def dense_gemm(x, w, x_scale=None, w_scale=None, out=None, ws=None):
 _U8, _BF16, _F32 = torch.uint8, torch.bfloat16, torch.float32
 
 
-def mxfp4_workspace_size(op: int, m: int, n: int, k: int) -> int:
-    """Workspace bytes of an MXFP4 call (MXFP4_GEMM: m, n, k; MXFP4_FFN: m, f, d)."""
-    return int(lib.sp24_mxfp4_workspace_size(op, m, n, k))
+def ffn_mxfp4_workspace_size(m: int, d: int, f: int) -> int:
+    """Workspace bytes of ffn_mxfp4 for m tokens."""
+    return int(lib.sp24_ffn_mxfp4_workspace_size(m, d, f))
 
 
 def mxfp4_scale_index(rows: int, cols: int, device=None) -> torch.Tensor:
@@ -773,21 +775,30 @@ def mxfp4_scale_index(rows: int, cols: int, device=None) -> torch.Tensor:
     return 4 * (4 * rows * (w // 4) + r * width + w % 4) + b % 4
 
 
+def _is(t, dtype, ndim, device):
+    """Whether a tensor passes _need (which then says what is wrong with it)."""
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == ndim and t.is_contiguous() and t.is_cuda
+            and (device is None or t.device == device))
+
+
 def _mx4_operand(codes, scales, name, device=None):
     """(rows, cols) of an MXFP4 operand: codes uint8 [rows, cols/2], scales uint8 of rows * cols/32."""
-    _need(codes, name + " codes", _U8, 2, device)
-    _need(scales, name + " scales", _U8, 1, codes.device)
-    rows, cols = codes.shape[0], 2 * codes.shape[1]
-    if cols % 128 or scales.numel() * 32 != rows * cols:
+    if not _is(codes, _U8, 2, device):
+        _need(codes, name + " codes", _U8, 2, device)
+    if not _is(scales, _U8, 1, codes.device):
+        _need(scales, name + " scales", _U8, 1, codes.device)
+    rows, half = codes.shape
+    if half % 64 or scales.numel() * 16 != rows * half:
         raise ValueError("%s: codes [%d, %d] need a multiple of 64 columns and %d scales, got %d"
-                         % (name, rows, cols // 2, rows * cols // 32, scales.numel()))
-    return rows, cols
+                         % (name, rows, half, rows * half // 16, scales.numel()))
+    return rows, 2 * half
 
 
 def _mx4_out(out, name, dtype, shape, device):
     if out is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    _need(out, name, dtype, len(shape), device)
+    if not _is(out, dtype, len(shape), device):
+        _need(out, name, dtype, len(shape), device)
     if out.shape != shape:
         raise ValueError("%s must be %s" % (name, list(shape)))
     return out
@@ -796,7 +807,8 @@ def _mx4_out(out, name, dtype, shape, device):
 def quant_mxfp4(x: torch.Tensor, out: torch.Tensor | None = None, scales: torch.Tensor | None = None):
     """bf16 [rows, cols] (cols % 128 == 0) -> MXFP4 (codes uint8 [rows, cols/2], scales uint8
     [rows * cols/32] in storage order, see mxfp4_scale_index)."""
-    _need(x, "x", _BF16, 2)
+    if not _is(x, _BF16, 2, None):
+        _need(x, "x", _BF16, 2)
     rows, cols = x.shape
     if cols % 128:
         raise ValueError("MXFP4 needs a multiple of 128 columns, got %d" % cols)
@@ -818,7 +830,7 @@ def dequant_mxfp4(codes: torch.Tensor, scales: torch.Tensor, out: torch.Tensor |
     return out
 
 
-def gemm_mxfp4(x_codes, x_scales, w_codes, w_scales, out=None, ws=None):
+def gemm_mxfp4(x_codes, x_scales, w_codes, w_scales, out=None):
     """Y = X . W^T of MXFP4 operands X [m, k] and W [n, k] (codes and scales of each); bf16 [m, n]."""
     m, k = _mx4_operand(x_codes, x_scales, "x")
     dev = x_codes.device
@@ -826,11 +838,9 @@ def gemm_mxfp4(x_codes, x_scales, w_codes, w_scales, out=None, ws=None):
     if kw != k:
         raise ValueError("w has %d columns, x has %d" % (kw, k))
     out = _mx4_out(out, "out", _BF16, (m, n), dev)
-    nbytes = lib.sp24_mxfp4_workspace_size(MXFP4_GEMM, m, n, k)
-    ws = _workspace(nbytes, dev, ws)
     _check("sp24_gemm_mxfp4", lib.sp24_gemm_mxfp4(m, n, k, x_codes.data_ptr(), x_scales.data_ptr(),
                                                   w_codes.data_ptr(), w_scales.data_ptr(), out.data_ptr(),
-                                                  None if ws is None else ws.data_ptr(), nbytes, _stream(dev)))
+                                                  _stream(dev)))
     return out
 
 
@@ -860,16 +870,20 @@ def gated_mxfp4(x_codes, x_scales, w_codes, w_scales, quantise=False, out=None, 
 
 
 def _norm_inputs(x, weight, residual, residual_out):
-    _need(x, "x", _BF16, 2)
+    if not _is(x, _BF16, 2, None):
+        _need(x, "x", _BF16, 2)
     m, k = x.shape
-    _need(weight, "weight", _BF16, 1, x.device)
+    dev = x.device
+    if not _is(weight, _BF16, 1, dev):
+        _need(weight, "weight", _BF16, 1, dev)
     if weight.numel() != k:
         raise ValueError("weight must hold %d values" % k)
     if residual is not None:
-        _need(residual, "residual", _BF16, 2, x.device)
+        if not _is(residual, _BF16, 2, dev):
+            _need(residual, "residual", _BF16, 2, dev)
         if residual.shape != x.shape:
             raise ValueError("residual must be [%d, %d]" % (m, k))
-        residual_out = _mx4_out(residual_out, "residual_out", _BF16, (m, k), x.device)
+        residual_out = _mx4_out(residual_out, "residual_out", _BF16, (m, k), dev)
     elif residual_out is not None:
         raise ValueError("residual_out goes with a residual")
     return m, k, residual_out
@@ -922,7 +936,7 @@ def ffn_mxfp4(x, weight, gu_codes, gu_scales, down_codes, down_scales, residual=
         raise ValueError("gate_up must be [%d, %d] values and down [%d, %d], got [%d, %d] and [%d, %d]"
                          % (2 * f, d, d, f, n2, kd, nd, f))
     out = _mx4_out(out, "out", _BF16, (m, d), dev)
-    nbytes = lib.sp24_mxfp4_workspace_size(MXFP4_FFN, m, f, d)
+    nbytes = lib.sp24_ffn_mxfp4_workspace_size(m, d, f)
     ws = _workspace(nbytes, dev, ws)
     _check("sp24_ffn_mxfp4", lib.sp24_ffn_mxfp4(
         m, d, f, x.data_ptr(), None if residual is None else residual.data_ptr(),

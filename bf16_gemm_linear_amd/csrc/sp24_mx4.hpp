@@ -123,12 +123,12 @@ struct Mx4Args {
   uint16_t* y;
   uint8_t* hq;
   uint32_t* hs;
-  float* partial;
 };
-size_t mx4_gemm_ws_bytes(int64_t m, int64_t n, int64_t k);  // split-K partial sums (not gated)
 hipError_t launch_mx4_gemm(const Mx4Args& a, hipStream_t s);
-// sp24_mx4_stream.hip, sp24_mx4_tiled.hip
+// The three kernels, by configuration (sp24_mx4_stream.hip: rb row blocks of 16 and `rows`
+// output columns a workgroup; sp24_mx4_wave.hip; sp24_mx4_tiled.hip).
 hipError_t launch_mx4_stream(int rb, int rows, const Mx4Args& a, hipStream_t s);
-hipError_t launch_mx4_tiled(int cfg, int split, const Mx4Args& a, hipStream_t s);
+hipError_t launch_mx4_wave(int cfg, const Mx4Args& a, hipStream_t s);
+hipError_t launch_mx4_tiled(int cfg, const Mx4Args& a, hipStream_t s);
 
 }  // namespace sp24

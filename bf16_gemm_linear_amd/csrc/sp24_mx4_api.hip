@@ -47,10 +47,9 @@ int quant_checks(const void* wide, int64_t rows, int64_t cols, const void* codes
   return bad ? SP24_ERR_ALIAS : SP24_OK;
 }
 
-// Workspace of the feed-forward block: the normed activation, the gated product and the
-// down-projection's own workspace.
+// Workspace of the feed-forward block: the normed activation and the gated product.
 struct FfnWs {
-  size_t xq, xs, hq, hs, gemm, gemm_bytes, total;
+  size_t xq, xs, hq, hs, total;
 };
 FfnWs ffn_ws(int64_t m, int64_t d, int64_t f) {
   FfnWs w;
@@ -58,9 +57,7 @@ FfnWs ffn_ws(int64_t m, int64_t d, int64_t f) {
   w.xs = w.xq + pad(code_bytes(m, d));
   w.hq = w.xs + pad(scale_bytes(m, d));
   w.hs = w.hq + pad(code_bytes(m, f));
-  w.gemm = w.hs + pad(scale_bytes(m, f));
-  w.gemm_bytes = mx4_gemm_ws_bytes(m, d, f);
-  w.total = w.gemm + w.gemm_bytes;
+  w.total = w.hs + pad(scale_bytes(m, f));
   return w;
 }
 
@@ -72,10 +69,8 @@ bool ffn_shape(int64_t m, int64_t d, int64_t f) {
 
 extern "C" {
 
-size_t sp24_mxfp4_workspace_size(int op, int64_t m, int64_t n, int64_t k) {
-  if (op == SP24_MXFP4_GEMM) return mx4_rows(m) && mx4_rows(n) && mx4_cols(k) ? mx4_gemm_ws_bytes(m, n, k) : 0;
-  if (op == SP24_MXFP4_FFN) return ffn_shape(m, k, n) ? ffn_ws(m, k, n).total : 0;
-  return 0;
+size_t sp24_ffn_mxfp4_workspace_size(int64_t m, int64_t d, int64_t f) {
+  return ffn_shape(m, d, f) ? ffn_ws(m, d, f).total : 0;
 }
 
 int sp24_quant_mxfp4(const void* x_bf16, int64_t rows, int64_t cols, uint8_t* codes_out, uint8_t* scales_out,
@@ -95,26 +90,19 @@ int sp24_dequant_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t rows
 }
 
 int sp24_gemm_mxfp4(int64_t m, int64_t n, int64_t k, const uint8_t* x_codes, const uint8_t* x_scales,
-                    const uint8_t* w_codes, const uint8_t* w_scales, void* y_bf16, void* ws, size_t ws_bytes,
-                    void* stream) {
+                    const uint8_t* w_codes, const uint8_t* w_scales, void* y_bf16, void* stream) {
   if (!x_codes || !x_scales || !w_codes || !w_scales || !y_bf16) return SP24_ERR_NULL;
   if (!mx4_rows(m) || !mx4_rows(n) || !mx4_cols(k)) return SP24_ERR_SHAPE;
   if (!aligned16(x_codes) || !aligned16(x_scales) || !aligned16(w_codes) || !aligned16(w_scales) ||
       !aligned16(y_bf16))
     return SP24_ERR_ALIGN;
-  const size_t need = mx4_gemm_ws_bytes(m, n, k);
-  if (need > 0) {
-    if (ws == nullptr || ws_bytes < need) return SP24_ERR_WORKSPACE;
-    if (!aligned16(ws)) return SP24_ERR_ALIGN;
-  }
   if (any_alias({{x_codes, code_bytes(m, k)}, {x_scales, scale_bytes(m, k)}, {w_codes, code_bytes(n, k)},
                  {w_scales, scale_bytes(n, k)}},
-                {Span{y_bf16, (size_t)m * n * 2}, Span{need > 0 ? ws : nullptr, need}}))
+                {Span{y_bf16, (size_t)m * n * 2}}))
     return SP24_ERR_ALIAS;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const Mx4Args a{(int)m, (int)n, (int)k, false, x_codes, reinterpret_cast<const uint32_t*>(x_scales), w_codes,
-                  reinterpret_cast<const uint32_t*>(w_scales), static_cast<uint16_t*>(y_bf16), nullptr, nullptr,
-                  static_cast<float*>(ws)};
+                  reinterpret_cast<const uint32_t*>(w_scales), static_cast<uint16_t*>(y_bf16), nullptr, nullptr};
   return finish(launch_mx4_gemm(a, s), s);
 }
 
@@ -136,7 +124,7 @@ int sp24_gated_mxfp4(int64_t m, int64_t f, int64_t k, const uint8_t* x_codes, co
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const Mx4Args a{(int)m, (int)f, (int)k, true, x_codes, reinterpret_cast<const uint32_t*>(x_scales), w_codes,
                   reinterpret_cast<const uint32_t*>(w_scales), static_cast<uint16_t*>(h_bf16), h_codes,
-                  reinterpret_cast<uint32_t*>(h_scales), nullptr};
+                  reinterpret_cast<uint32_t*>(h_scales)};
   return finish(launch_mx4_gemm(a, s), s);
 }
 
@@ -208,11 +196,11 @@ int sp24_ffn_mxfp4(int64_t m, int64_t d, int64_t f, const void* x_bf16, const vo
                                          static_cast<const uint16_t*>(weight_bf16), eps, b + w.xq, xs}, s);
   if (e == hipSuccess)
     e = launch_mx4_gemm(Mx4Args{(int)m, (int)f, (int)d, true, b + w.xq, xs, gu_codes,
-                                reinterpret_cast<const uint32_t*>(gu_scales), nullptr, b + w.hq, hs, nullptr}, s);
+                                reinterpret_cast<const uint32_t*>(gu_scales), nullptr, b + w.hq, hs}, s);
   if (e == hipSuccess)
     e = launch_mx4_gemm(Mx4Args{(int)m, (int)d, (int)f, false, b + w.hq, hs, down_codes,
                                 reinterpret_cast<const uint32_t*>(down_scales), static_cast<uint16_t*>(y_bf16), nullptr,
-                                nullptr, reinterpret_cast<float*>(b + w.gemm)}, s);
+                                nullptr}, s);
   return finish(e, s);
 }
 

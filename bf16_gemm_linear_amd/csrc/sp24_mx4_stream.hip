@@ -1,45 +1,49 @@
 // Products of MXFP4 operands for few tokens (decode): the weight's bytes are the time.
 //
 // A workgroup owns up to 16 RBK rows of W (gated: half of them gate rows, half their up
-// rows) and all of K, split over its KW waves in steps of U units of 128 values; the waves' sums are
-// joined through LDS in a fixed order.  Codes go from memory straight into registers, 1 KB
-// an instruction (16 rows x 64 contiguous bytes), D steps ahead: at the sizes of a decode
-// step that is most of the workgroup's share of W in flight at once, which is what hides
-// the latency.  W is read once, with the non-temporal hint; X comes from L2.
+// rows) and all of K.  Its KW waves take turns at steps of 256 values and never wait for
+// each other: each wave has its own ring of S buffers in LDS, loads a step of W, X and
+// their scales straight into it (global_load_lds: whole 128-byte lines of 8 rows an
+// instruction), S - 1 steps ahead, and waits only for its own loads.  The rings together
+// hold most of a decode step's share of W in flight, which is what hides the latency, and
+// a wave's chain of waits is 1 / KW of the steps.  The waves' sums are joined through LDS
+// in a fixed order.  W is read once, with the non-temporal hint; X comes from L2.
 //
 // v_mfma_scale_f32_16x16x128_f8f6f4: lane l holds row l % 16 (A: W, B: X) and block l / 16
 // of the unit's four, so its scale is byte l / 16 of the row's word; accumulator register e
-// is W row 4 (l / 16) + e, token l % 16.  Rows and units that do not exist read as zero
-// codes through the buffer's range check (no memory is touched); their scales are those of
-// a row or unit that does exist, so a product with them is 0, and NaN only where the row's
-// own result is.
+// is W row 4 (l / 16) + e, token l % 16.  Rows past the last are the last one again, and
+// where fewer than 16 tokens are loaded (XR = 8) they stand for the others: their outputs
+// are not stored.
+#include "sp24_dma.hpp"
 #include "sp24_mx4.hpp"
 
 namespace sp24 {
 namespace {
 
-enum { PLAIN = 0, GATED_BF16 = 2, GATED_MX4 = 3 };
+enum { PLAIN = 0, GATED_BF16 = 1, GATED_MX4 = 2 };
 
-constexpr int kNonTemporal = 2;
+constexpr int KS = 256, RB = KS / 2, P = RB / 16, SW = KS / 128;  // a step: bytes, pieces, scale words of a row
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, size_t bytes) {
-  const uint32_t n = bytes < 0x7FFFFFF0u ? (uint32_t)bytes : 0x7FFFFFF0u;
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)n, 0x00020000);
-}
-
-// One step: U units of 128 values, codes and scale words of the wave's row and token blocks.
-template <int RBK, int MB, int U>
-struct Step {
-  i32x4 w[RBK][U], x[MB][U];
-  uint32_t ws[RBK][U], xs[MB][U];
+template <int RBK_, int MB_, int XR_, int KW_, int S_>
+struct StreamCfg {
+  static constexpr int RBK = RBK_, MB = MB_, XR = XR_, KW = KW_, S = S_;
+  static constexpr int R = 16 * RBK;
+  static constexpr int W_I = R / 8, X_I = XR / 8, S_I = (R + XR + 31) / 32;  // load instructions of a step
+  static constexpr int PER = W_I + X_I + S_I;
+  static constexpr int X_OFF = R * RB, S_OFF = X_OFF + XR * RB, STAGE = S_OFF + S_I * 256;
+  static constexpr int RED = KW * RBK * MB * 1024;
+  static constexpr int LDS = KW * S * STAGE > RED ? KW * S * STAGE : RED;
+  static_assert(LDS <= 160 * 1024 && (S - 1) * PER < 64, "LDS and counter range");
+  static_assert(XR % 8 == 0 && XR <= 16 * MB && (XR == 16 * MB || XR == 8), "token rows");
 };
 
 // rows: output columns of a workgroup (a multiple of 4; of 32 for GATED_MX4).
-template <int RBK, int MB, int KW, int U, int D, int MODE>
-__global__ __launch_bounds__(KW * 64) void mx4_stream_kernel(Mx4Args p, int rows) {
+template <class C, int MODE>
+__global__ __launch_bounds__(C::KW * 64, C::KW / 4) void mx4_stream_kernel(Mx4Args p, int rows) {
   constexpr bool GATED = MODE != PLAIN;
+  constexpr int RBK = C::RBK, MB = C::MB, KW = C::KW, S = C::S;
   constexpr int OB = GATED ? RBK / 2 : RBK;  // row blocks of the output
-  __shared__ __attribute__((aligned(16))) f32x4 red[KW][RBK * MB][64];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[C::LDS];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int kw = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -47,25 +51,57 @@ __global__ __launch_bounds__(KW * 64) void mx4_stream_kernel(Mx4Args p, int rows
   const int n0 = blockIdx.x * rows, nrows = min(rows, p.n - n0);
   const int m0 = blockIdx.y * 16 * MB, mrows = min(16 * MB, p.m - m0);
   const size_t half = (size_t)p.k / 2;
-  const int words = p.k / 128, nsteps = (words + U - 1) / U;
+  const int words = p.k / 128, nsteps = (words + SW - 1) / SW;
   const int wrows = GATED ? 2 * p.n : p.n;
+  uint8_t* ring = lds + kw * (S * C::STAGE);
 
-  // rows past the range (rows need not be a multiple of 16) are past the buffer's end
-  const __amdgpu_buffer_rsrc_t wb0 = buffer(p.w + (size_t)n0 * half, nrows * half);
-  const __amdgpu_buffer_rsrc_t wb1 = GATED ? buffer(p.w + (size_t)(p.n + n0) * half, nrows * half) : wb0;
-  const __amdgpu_buffer_rsrc_t xb = buffer(p.x + (size_t)m0 * half, mrows * half);
-  uint32_t woff[OB], xoff[MB];
-  int wsr[RBK], xsr[MB];
+  // per-lane offsets of this wave's loads from uniform bases; LDS row i of W is output
+  // column i % (16 OB) of the gate (i < 16 OB) or up half
+  const uint8_t* const w0 = p.w + (size_t)n0 * half;
+  const uint8_t* const w1 = GATED ? p.w + (size_t)(p.n + n0) * half : w0;
+  const uint8_t* const x0 = p.x + (size_t)m0 * half;
+  uint32_t woff[C::W_I], xoff[C::X_I], past[2];
+  int srow[C::S_I];
 #pragma unroll
-  for (int i = 0; i < OB; ++i) woff[i] = (uint32_t)(16 * i + r) * (uint32_t)half + 16 * q;
-#pragma unroll
-  for (int i = 0; i < RBK; ++i)
-    wsr[i] = n0 + min(16 * (i % OB) + r, nrows - 1) + (i >= OB ? p.n : 0);
-#pragma unroll
-  for (int j = 0; j < MB; ++j) {
-    xoff[j] = (uint32_t)(16 * j + r) * (uint32_t)half + 16 * q;
-    xsr[j] = m0 + min(16 * j + r, mrows - 1);
+  for (int j = 0; j < C::W_I; ++j) {
+    const int row = 8 * j + lane / P;
+    woff[j] = (uint32_t)min(row % (16 * OB), nrows - 1) * (uint32_t)half + 16 * swz16<P>(row, lane % P);
   }
+#pragma unroll
+  for (int j = 0; j < C::X_I; ++j) {
+    const int row = 8 * j + lane / P;
+    xoff[j] = (uint32_t)min(row, mrows - 1) * (uint32_t)half + 16 * swz16<P>(row, lane % P);
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j) past[j] = swz16<P>(8 * j + lane / P, lane % P) >= P / 2 ? RB / 2 : 0;
+#pragma unroll
+  for (int j = 0; j < C::S_I; ++j) {
+    const int row = min(32 * j + lane / SW, C::R + C::XR - 1);
+    srow[j] = row < C::R ? n0 + min(row % (16 * OB), nrows - 1) + (row >= 16 * OB ? p.n : 0)
+                         : m0 + min(row - C::R, mrows - 1);
+  }
+
+  // Step ks into buffer b.  A step that reaches past k loads its first half twice: the
+  // second copy stays unread, and no load leaves its row.
+  auto issue = [&](int b, int ks) {
+    uint8_t* buf = ring + b * C::STAGE;
+    const bool over = ks * SW + 1 >= words;  // uniform
+    const int w = ks * SW, blk = w / 4, width = min(4, words - 4 * blk);
+#pragma unroll
+    for (int j = 0; j < C::W_I; ++j)
+      dma16_nt((j < 2 * OB ? w0 : w1) + (size_t)ks * RB + (woff[j] - (over ? past[j & 1] : 0)), buf + j * 1024);
+#pragma unroll
+    for (int j = 0; j < C::X_I; ++j)
+      dma16(x0 + (size_t)ks * RB + (xoff[j] - (over ? past[j & 1] : 0)), buf + C::X_OFF + j * 1024);
+#pragma unroll
+    for (int j = 0; j < C::S_I; ++j) {
+      const uint32_t* ws = p.ws + (size_t)4 * wrows * blk + w % 4;
+      const uint32_t* xs = p.xs + (size_t)4 * p.m * blk + w % 4;
+      // an instruction can hold rows of both operands
+      const uint32_t* base = 32 * j + 31 < C::R ? ws : 32 * j >= C::R ? xs : 32 * j + lane / SW < C::R ? ws : xs;
+      dma4(base + ((uint32_t)srow[j] * (uint32_t)width + (over ? 0 : lane % SW)), buf + C::S_OFF + j * 256);
+    }
+  };
 
   f32x4 acc[RBK][MB];
 #pragma unroll
@@ -73,75 +109,57 @@ __global__ __launch_bounds__(KW * 64) void mx4_stream_kernel(Mx4Args p, int rows
 #pragma unroll
     for (int j = 0; j < MB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  // step t of this wave: units U (kw + KW t) and the next
-  auto load = [&](Step<RBK, MB, U>& s, int t) {
-    const int step = kw + KW * t;
-    uint32_t k[U];
+  const int cnt = nsteps > kw ? (nsteps - kw + KW - 1) / KW : 0;  // steps of this wave: kw + KW t
 #pragma unroll
-    for (int u = 0; u < U; ++u) k[u] = U * step + u < words ? (uint32_t)(U * step + u) * 64u : 0x80000000u;
-    const int w = U * min(step, nsteps - 1), b = w / 4, width = min(4, words - 4 * b);
-    const bool both = w + 1 < words;
-    auto scales = [&](const uint32_t* base, int rows_all, const int* row, auto* out, int count) {
-      const __amdgpu_buffer_rsrc_t sb = buffer(base + (size_t)4 * rows_all * b, (size_t)rows_all * width * 4);
+  for (int t = 0; t < S; ++t)
+    if (t < cnt) issue(t, kw + KW * t);
+  int b = 0;
+  for (int t = 0; t < cnt; ++t) {
+    wait_later<C::PER, S - 1>(min(cnt - 1 - t, S - 1));
+    asm volatile("" ::: "memory");
+    const uint8_t* buf = ring + b * C::STAGE;
+    i32x4 a[RBK][SW], x[MB][SW];
+    int sa[RBK][SW], sx[MB][SW];
 #pragma unroll
-      for (int i = 0; i < count; ++i) {
-        const uint32_t off = ((uint32_t)row[i] * (uint32_t)width + w % 4) * 4u;
-        if constexpr (U == 2) {  // a row's last word alone: the second is another row's, or past the end
-          const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(sb, off, 0, 0));
-          out[i][0] = v[0];
-          out[i][1] = both ? v[1] : v[0];
-        } else {
-          out[i][0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_raw_buffer_load_b32(sb, off, 0, 0));
-        }
-      }
-    };
-#pragma unroll
-    for (int i = 0; i < RBK; ++i)
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        s.w[i][u] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                  i < OB ? wb0 : wb1, k[u] + woff[i % OB], 0, kNonTemporal));
-    scales(p.ws, wrows, wsr, s.ws, RBK);
-#pragma unroll
-    for (int j = 0; j < MB; ++j)
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        s.x[j][u] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(xb, k[u] + xoff[j], 0, 0));
-    scales(p.xs, p.m, xsr, s.xs, MB);
-  };
-  auto compute = [&](const Step<RBK, MB, U>& s) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      int sx[MB];
-#pragma unroll
-      for (int j = 0; j < MB; ++j) sx[j] = (int)(s.xs[j][u] >> (8 * q));
+    for (int u = 0; u < SW; ++u) {
 #pragma unroll
       for (int i = 0; i < RBK; ++i) {
-        const int sw = (int)(s.ws[i][u] >> (8 * q));
-        const i32x8 a = __builtin_shufflevector(s.w[i][u], s.w[i][u], 0, 1, 2, 3, -1, -1, -1, -1);
+        const int row = 16 * i + r;
+        a[i][u] = *reinterpret_cast<const i32x4*>(buf + row * RB + 16 * swz16<P>(row, 4 * u + q));
+        sa[i][u] = buf[C::S_OFF + row * 8 + 4 * u + q];
+      }
+#pragma unroll
+      for (int j = 0; j < MB; ++j) {
+        const int row = (16 * j + r) % C::XR;
+        x[j][u] = *reinterpret_cast<const i32x4*>(buf + C::X_OFF + row * RB + 16 * swz16<P>(row, 4 * u + q));
+        sx[j][u] = buf[C::S_OFF + (C::R + row) * 8 + 4 * u + q];
+      }
+    }
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the buffer is read, and may be filled again
+    __builtin_amdgcn_sched_barrier(0);
+    const int ks = kw + KW * t;
+    if (t + S < cnt) issue(b, ks + KW * S);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int u = 0; u < SW; ++u) {
+      if (u > 0 && ks * SW + u >= words) break;  // uniform: the last step holds 128 values
+#pragma unroll
+      for (int i = 0; i < RBK; ++i) {
+        const i32x8 a8 = __builtin_shufflevector(a[i][u], a[i][u], 0, 1, 2, 3, -1, -1, -1, -1);
 #pragma unroll
         for (int j = 0; j < MB; ++j) {
-          const i32x8 b = __builtin_shufflevector(s.x[j][u], s.x[j][u], 0, 1, 2, 3, -1, -1, -1, -1);
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc[i][j], 4, 4, 0, sw, 0, sx[j]);
+          const i32x8 x8 = __builtin_shufflevector(x[j][u], x[j][u], 0, 1, 2, 3, -1, -1, -1, -1);
+          acc[i][j] =
+              __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a8, x8, acc[i][j], 4, 4, 0, sa[i][u], 0, sx[j][u]);
         }
       }
     }
-  };
-
-  const int cnt = (nsteps - kw + KW - 1) / KW;  // steps of this wave (0 where nsteps <= kw)
-  Step<RBK, MB, U> st[D];
-#pragma unroll
-  for (int d = 0; d < D; ++d) load(st[d], d);
-  for (int t = 0; t + D < cnt; t += D) {
-#pragma unroll
-    for (int d = 0; d < D; ++d) {
-      compute(st[d]);
-      load(st[d], t + d + D);
-    }
+    b = b + 1 == S ? 0 : b + 1;
   }
-#pragma unroll
-  for (int d = 0; d < D; ++d) compute(st[d]);
 
+  // the rings are free behind the barrier; tile (i, j) of wave kw at red[kw][i MB + j]
+  f32x4(*red)[RBK * MB][64] = reinterpret_cast<f32x4(*)[RBK * MB][64]>(lds);
+  __syncthreads();
 #pragma unroll
   for (int i = 0; i < RBK; ++i)
 #pragma unroll
@@ -172,7 +190,7 @@ __global__ __launch_bounds__(KW * 64) void mx4_stream_kernel(Mx4Args p, int rows
       key = max(key, (uint32_t)__shfl_xor((int)key, 32, 64));
       const uint32_t byte = mx4_scale_byte(key >> 23, key == 0), c8 = mx4_codes8(v, byte);
       const int m = m0 + 16 * j + (l & 15), n = n0 + 32 * blk, qq = l >> 4;
-      if (m >= p.m || n >= p.n) continue;
+      if (m >= p.m || 32 * blk >= nrows) continue;  // rows past the range are the next workgroup's
       uint16_t* o = reinterpret_cast<uint16_t*>(p.hq + (size_t)m * (p.n / 2) + n / 2) + qq;
       o[0] = (uint16_t)c8;
       o[4] = (uint16_t)(c8 >> 16);
@@ -203,35 +221,46 @@ __global__ __launch_bounds__(KW * 64) void mx4_stream_kernel(Mx4Args p, int rows
   }
 }
 
-template <int RBK, int MB, int KW, int U, int D>
+template <int RBK, int MB, int XR, int KW, int S>
 hipError_t launch(const Mx4Args& a, int rows, hipStream_t s) {
+  using C = StreamCfg<RBK, MB, XR, KW, S>;
   const dim3 grid((a.n + rows - 1) / rows, (a.m + 16 * MB - 1) / (16 * MB));
   if (!a.gated) {
-    hipLaunchKernelGGL((mx4_stream_kernel<RBK, MB, KW, U, D, PLAIN>), grid, dim3(KW * 64), 0, s, a, rows);
-  } else if constexpr (RBK % 2 == 0) {
-    if (a.hq == nullptr) {
-      hipLaunchKernelGGL((mx4_stream_kernel<RBK, MB, KW, U, D, GATED_BF16>), grid, dim3(KW * 64), 0, s, a, rows);
-    } else if constexpr (RBK == 4) {
-      hipLaunchKernelGGL((mx4_stream_kernel<RBK, MB, KW, U, D, GATED_MX4>), grid, dim3(KW * 64), 0, s, a, rows);
-    }
+    hipLaunchKernelGGL((mx4_stream_kernel<C, PLAIN>), grid, dim3(KW * 64), 0, s, a, rows);
+    return hipGetLastError();
   }
-  return hipGetLastError();
+  if (a.hq == nullptr) {
+    if constexpr (RBK % 2 == 0) {
+      hipLaunchKernelGGL((mx4_stream_kernel<C, GATED_BF16>), grid, dim3(KW * 64), 0, s, a, rows);
+      return hipGetLastError();
+    }
+  } else if constexpr (RBK % 4 == 0) {
+    hipLaunchKernelGGL((mx4_stream_kernel<C, GATED_MX4>), grid, dim3(KW * 64), 0, s, a, rows);
+    return hipGetLastError();
+  }
+  return hipErrorInvalidConfiguration;  // never planned: too few row blocks for this output
 }
 
 }  // namespace
 
 hipError_t launch_mx4_stream(int rb, int rows, const Mx4Args& a, hipStream_t s) {
-  const int mb = a.m <= 16 ? 1 : a.m <= 32 ? 2 : 4;
+  const int mb = a.m <= 8 ? 0 : a.m <= 16 ? 1 : a.m <= 32 ? 2 : 4;
   switch (10 * rb + mb) {
-    case 11: return launch<1, 1, 8, 2, 4>(a, rows, s);
-    case 12: return launch<1, 2, 8, 2, 3>(a, rows, s);
-    case 14: return launch<1, 4, 8, 1, 4>(a, rows, s);
-    case 21: return launch<2, 1, 8, 2, 2>(a, rows, s);
-    case 22: return launch<2, 2, 8, 2, 2>(a, rows, s);
-    case 24: return launch<2, 4, 8, 1, 3>(a, rows, s);
-    case 41: return launch<4, 1, 8, 2, 2>(a, rows, s);
-    case 42: return launch<4, 2, 8, 1, 3>(a, rows, s);
-    default: return launch<4, 4, 8, 1, 2>(a, rows, s);
+    case 10: return launch<1, 1, 8, 8, 4>(a, rows, s);
+    case 11: return launch<1, 1, 16, 8, 4>(a, rows, s);
+    case 12: return launch<1, 2, 32, 8, 2>(a, rows, s);
+    case 14: return launch<1, 4, 64, 4, 3>(a, rows, s);
+    case 20: return launch<2, 1, 8, 8, 3>(a, rows, s);
+    case 21: return launch<2, 1, 16, 8, 2>(a, rows, s);
+    case 22: return launch<2, 2, 32, 8, 2>(a, rows, s);
+    case 24: return launch<2, 4, 64, 4, 3>(a, rows, s);
+    case 40: return launch<4, 1, 8, 8, 2>(a, rows, s);
+    case 41: return launch<4, 1, 16, 4, 3>(a, rows, s);
+    case 42: return launch<4, 2, 32, 4, 3>(a, rows, s);
+    case 44: return launch<4, 4, 64, 4, 2>(a, rows, s);
+    case 80: return launch<8, 1, 8, 4, 2>(a, rows, s);
+    case 81: return launch<8, 1, 16, 4, 2>(a, rows, s);
+    default: return hipErrorInvalidConfiguration;
   }
 }
 

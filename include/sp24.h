@@ -488,11 +488,9 @@ int sp24_dequant_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t rows
  *   x_codes [m, k/2], x_scales m*k/32 bytes; w_codes [n, k/2], w_scales n*k/32
  *   bytes; y_bf16 [m, n].
  * Requires m, n >= 1, at most 2^21; 128 <= k <= 2^24, k % 128 == 0.  The sum over k is formed in a fixed order for a given (m, n, k): results
- * are bitwise reproducible.  ws/ws_bytes: sp24_mxfp4_workspace_size(
- * SP24_MXFP4_GEMM, m, n, k). */
+ * are bitwise reproducible.  No workspace. */
 int sp24_gemm_mxfp4(int64_t m, int64_t n, int64_t k, const uint8_t* x_codes, const uint8_t* x_scales,
-                    const uint8_t* w_codes, const uint8_t* w_scales, void* y_bf16, void* ws, size_t ws_bytes,
-                    void* stream);
+                    const uint8_t* w_codes, const uint8_t* w_scales, void* y_bf16, void* stream);
 
 /* The gated projection of a feed-forward block in one kernel:
  *   h = silu(X Wg^T) * (X Wu^T),  silu(g) = g / (1 + exp(-g)),
@@ -539,28 +537,22 @@ int sp24_rmsnorm(int kind, int64_t m, int64_t k, int64_t group, const void* x_bf
                  void* residual_out_bf16, const void* weight_bf16, float eps, void* out, void* scales_out,
                  void* stream);
 
-/* A pre-norm feed-forward block in MXFP4, three launches (four where the last
- * product splits k): X + residual normed into MXFP4 (sp24_rmsnorm), the gated
+/* A pre-norm feed-forward block in MXFP4, three launches: X + residual normed into MXFP4 (sp24_rmsnorm), the gated
  * projection with an MXFP4 output (sp24_gated_mxfp4), the down-projection
  * (sp24_gemm_mxfp4); bit for bit those calls in turn.
  *   x_bf16, residual_bf16 (or NULL), residual_out_bf16, weight_bf16 [d], eps as
  *   sp24_rmsnorm; gu_codes [2f, d/2] and gu_scales as sp24_gated_mxfp4; down_codes
  *   [d, f/2], down_scales d*f/32 bytes; y_bf16 [m, d] (the residual is not added).
  * Requires d % 128 == 0, d <= 65536, f % 128 == 0 and the limits of the three
- * calls.  ws/ws_bytes: sp24_mxfp4_workspace_size(SP24_MXFP4_FFN, m, f, d). */
+ * calls.  ws/ws_bytes: sp24_ffn_mxfp4_workspace_size(m, d, f). */
 int sp24_ffn_mxfp4(int64_t m, int64_t d, int64_t f, const void* x_bf16, const void* residual_bf16,
                    void* residual_out_bf16, const void* weight_bf16, float eps, const uint8_t* gu_codes,
                    const uint8_t* gu_scales, const uint8_t* down_codes, const uint8_t* down_scales, void* y_bf16,
                    void* ws, size_t ws_bytes, void* stream);
 
-typedef enum sp24_mxfp4_op {
-  SP24_MXFP4_GEMM = 0, /* sp24_gemm_mxfp4 (m, n, k) */
-  SP24_MXFP4_FFN = 1   /* sp24_ffn_mxfp4 (m, n = f, k = d) */
-} sp24_mxfp4_op;
-
-/* Workspace bytes of an MXFP4 call (0 if none; also 0 for invalid arguments,
- * which the call itself then rejects).  Host-only. */
-size_t sp24_mxfp4_workspace_size(int op, int64_t m, int64_t n, int64_t k);
+/* Workspace bytes of sp24_ffn_mxfp4 (0 for invalid sizes, which the call itself
+ * then rejects).  Host-only. */
+size_t sp24_ffn_mxfp4_workspace_size(int64_t m, int64_t d, int64_t f);
 
 /* Workspace bytes needed by an op at a shape (0 if none; also 0 for invalid
  * arguments, which the op itself then rejects). */

@@ -113,6 +113,41 @@ def test_gemm_against_oracle(m, n, k):
     assert np.array_equal(bits(y), bits(y2))
 
 
+# every configuration of the three kernels, at sizes around its tiles and with whole, half and
+# few steps of K (the override picks it wherever it can run the call)
+CONFIGS = ["stream,1", "stream,2", "stream,4", "stream,8"] + ["wave,%d" % i for i in range(6)] + \
+    ["tiled,%d" % i for i in range(6)]
+
+
+@pytest.mark.parametrize("config", CONFIGS)
+def test_every_configuration(config, monkeypatch):
+    sp = need_sp()
+    monkeypatch.setenv("SP24_MX4", config)
+    for m in ((1, 9, 16, 17, 33, 64) if config.startswith("stream") else (1, 31, 64, 65, 127, 129, 257)):
+        for n, k in ((1, 128), (30, 640), (129, 1024), (256, 256), (260, 1408), (384, 2560)):
+            announce(config, m, n, k)
+            (xc, xs), x = operand(m, k, m + k)
+            (wc, ws), w = operand(n, k, n + k + 7, 0.05)
+            y = torch.full((m, n), float("nan"), dtype=torch.bfloat16, device=DEV)
+            sp.gemm_mxfp4(xc, xs, wc, ws, out=y)
+            torch.cuda.synchronize()
+            ref, mag = R.gemm_ref(x, w)
+            got = bf16_to_f64(bits(y))
+            assert (np.abs(got - ref) <= 2.0 ** -8 * np.abs(ref) + ACC * mag).all(), (m, n, k)
+            if n % 2:
+                continue
+            f = n // 2
+            ref, err = R.gated_ref(x, w)
+            err = ACC * err + 2.0 ** -16 * np.abs(ref)
+            h = sp.gated_mxfp4(xc, xs, wc, ws)
+            torch.cuda.synchronize()
+            assert (np.abs(bf16_to_f64(bits(h)) - ref) <= 2.0 ** -8 * np.abs(ref) + err).all(), (m, n, k)
+            if f % 128 == 0:
+                c, s = sp.gated_mxfp4(xc, xs, wc, ws, quantise=True)
+                torch.cuda.synchronize()
+                check_mx4_output(c, s, ref, err, (m, n, k))
+
+
 def test_gemm_extreme_scales_and_nan():
     """Scales from 2^-127 to 2^100 with products in range, and one row of X and one of W with a NaN block."""
     sp = need_sp()
@@ -223,7 +258,7 @@ def test_calls_on_another_stream_and_in_a_graph():
     dn = sp.quant_mxfp4(W.randn_bf16((d, f), 4, 0.05).to(DEV))
     w = W.randn_bf16((d,), 9).to(DEV)
     xs = [W.randn_bf16((m, d), 20 + i).to(DEV) for i in range(5)]
-    ws = torch.empty(sp.mxfp4_workspace_size(sp.MXFP4_FFN, m, f, d), dtype=torch.uint8, device=DEV)
+    ws = torch.empty(sp.ffn_mxfp4_workspace_size(m, d, f), dtype=torch.uint8, device=DEV)
     want = [sp.ffn_mxfp4(x, w, *gu, *dn)[0].clone() for x in xs]
     x, y = xs[0].clone(), torch.empty(m, d, dtype=torch.bfloat16, device=DEV)
     torch.cuda.synchronize()
