@@ -1,8 +1,10 @@
 """Python binding of libsp24: 2:4 structured-sparse GEMM for gfx950 (MI355X).
 
-Thin ctypes marshalling over the C ABI declared in include/sp24.h: every call
-checks dtypes, devices, shapes and contiguity of torch tensors, passes their
-device pointers and the current HIP stream, and raises on a non-OK status.
+Thin marshalling over the C ABI declared in include/sp24.h (ctypes; the MXFP4
+operators and the norm, whose kernels are shorter than a call through ctypes, in
+the C++ module _sp24): every call checks dtypes, devices, shapes and contiguity
+of torch tensors, passes their device pointers and the current HIP stream, and
+raises on a non-OK status.
 PyTorch is used only for device memory and streams; all arithmetic runs in the
 library's HIP kernels.  If libsp24.so is missing this module raises on import:
 there is no fallback.
@@ -123,10 +125,19 @@ lib.sp24_ffn_mxfp4_workspace_size.restype = _sz
 lib.sp24_status_string.restype = ctypes.c_char_p
 
 
+try:  # the binding of the MXFP4 operators and the norm, in C++ (csrc/sp24_python.cpp)
+    from . import _sp24 as _native
+except ImportError as _e:
+    raise ImportError("%s: it is built with libsp24.so by `python bf16_gemm_linear_amd/build.py`" % _e) from _e
+
+
 class Sp24Error(RuntimeError):
     def __init__(self, fn, status):
         self.status = status
         super().__init__("%s failed: %s (%d)" % (fn, lib.sp24_status_string(status).decode(), status))
+
+
+_native.set_error(Sp24Error)
 
 
 def _check(fn, status):
@@ -754,9 +765,6 @@ def dense_gemm(x, w, x_scale=None, w_scale=None, out=None, ws=None):
 
 # --------------------------------------------------------------------------- probes
 
-_U8, _BF16, _F32 = torch.uint8, torch.bfloat16, torch.float32
-
-
 def ffn_mxfp4_workspace_size(m: int, d: int, f: int) -> int:
     """Workspace bytes of ffn_mxfp4 for m tokens."""
     return int(lib.sp24_ffn_mxfp4_workspace_size(m, d, f))
@@ -775,118 +783,26 @@ def mxfp4_scale_index(rows: int, cols: int, device=None) -> torch.Tensor:
     return 4 * (4 * rows * (w // 4) + r * width + w % 4) + b % 4
 
 
-def _is(t, dtype, ndim, device):
-    """Whether a tensor passes _need (which then says what is wrong with it)."""
-    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == ndim and t.is_contiguous() and t.is_cuda
-            and (device is None or t.device == device))
-
-
-def _mx4_operand(codes, scales, name, device=None):
-    """(rows, cols) of an MXFP4 operand: codes uint8 [rows, cols/2], scales uint8 of rows * cols/32."""
-    if not _is(codes, _U8, 2, device):
-        _need(codes, name + " codes", _U8, 2, device)
-    if not _is(scales, _U8, 1, codes.device):
-        _need(scales, name + " scales", _U8, 1, codes.device)
-    rows, half = codes.shape
-    if half % 64 or scales.numel() * 16 != rows * half:
-        raise ValueError("%s: codes [%d, %d] need a multiple of 64 columns and %d scales, got %d"
-                         % (name, rows, half, rows * half // 16, scales.numel()))
-    return rows, 2 * half
-
-
-def _mx4_out(out, name, dtype, shape, device):
-    if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if not _is(out, dtype, len(shape), device):
-        _need(out, name, dtype, len(shape), device)
-    if out.shape != shape:
-        raise ValueError("%s must be %s" % (name, list(shape)))
-    return out
-
-
 def quant_mxfp4(x: torch.Tensor, out: torch.Tensor | None = None, scales: torch.Tensor | None = None):
     """bf16 [rows, cols] (cols % 128 == 0) -> MXFP4 (codes uint8 [rows, cols/2], scales uint8
     [rows * cols/32] in storage order, see mxfp4_scale_index)."""
-    if not _is(x, _BF16, 2, None):
-        _need(x, "x", _BF16, 2)
-    rows, cols = x.shape
-    if cols % 128:
-        raise ValueError("MXFP4 needs a multiple of 128 columns, got %d" % cols)
-    dev = x.device
-    out = _mx4_out(out, "out", _U8, (rows, cols // 2), dev)
-    scales = _mx4_out(scales, "scales", _U8, (rows * cols // 32,), dev)
-    _check("sp24_quant_mxfp4", lib.sp24_quant_mxfp4(x.data_ptr(), rows, cols, out.data_ptr(), scales.data_ptr(),
-                                                    _stream(dev)))
-    return out, scales
+    return _native.quant(x, out, scales)
 
 
 def dequant_mxfp4(codes: torch.Tensor, scales: torch.Tensor, out: torch.Tensor | None = None):
     """The bf16 values [rows, cols] that MXFP4 codes and scales stand for (exact)."""
-    rows, cols = _mx4_operand(codes, scales, "operand")
-    dev = codes.device
-    out = _mx4_out(out, "out", _BF16, (rows, cols), dev)
-    _check("sp24_dequant_mxfp4", lib.sp24_dequant_mxfp4(codes.data_ptr(), scales.data_ptr(), rows, cols,
-                                                        out.data_ptr(), _stream(dev)))
-    return out
+    return _native.dequant(codes, scales, out)
 
 
 def gemm_mxfp4(x_codes, x_scales, w_codes, w_scales, out=None):
     """Y = X . W^T of MXFP4 operands X [m, k] and W [n, k] (codes and scales of each); bf16 [m, n]."""
-    m, k = _mx4_operand(x_codes, x_scales, "x")
-    dev = x_codes.device
-    n, kw = _mx4_operand(w_codes, w_scales, "w", dev)
-    if kw != k:
-        raise ValueError("w has %d columns, x has %d" % (kw, k))
-    out = _mx4_out(out, "out", _BF16, (m, n), dev)
-    _check("sp24_gemm_mxfp4", lib.sp24_gemm_mxfp4(m, n, k, x_codes.data_ptr(), x_scales.data_ptr(),
-                                                  w_codes.data_ptr(), w_scales.data_ptr(), out.data_ptr(),
-                                                  _stream(dev)))
-    return out
+    return _native.gemm(x_codes, x_scales, w_codes, w_scales, out)
 
 
 def gated_mxfp4(x_codes, x_scales, w_codes, w_scales, quantise=False, out=None, out_scales=None):
     """silu(X Wg^T) * (X Wu^T) of MXFP4 operands, W = [f gate rows; f up rows]: bf16 [m, f], or with
     quantise=True (f % 128 == 0) MXFP4 (codes, scales), the X of the next gemm_mxfp4."""
-    m, k = _mx4_operand(x_codes, x_scales, "x")
-    dev = x_codes.device
-    n, kw = _mx4_operand(w_codes, w_scales, "w", dev)
-    if kw != k or n % 2:
-        raise ValueError("w must be [2 f, %d] values, got [%d, %d]" % (k, n, kw))
-    f = n // 2
-    if quantise:
-        if f % 128:
-            raise ValueError("an MXFP4 output needs a multiple of 128 columns, got %d" % f)
-        out = _mx4_out(out, "out", _U8, (m, f // 2), dev)
-        out_scales = _mx4_out(out_scales, "out_scales", _U8, (m * f // 32,), dev)
-    else:
-        if out_scales is not None:
-            raise ValueError("out_scales goes with quantise=True")
-        out = _mx4_out(out, "out", _BF16, (m, f), dev)
-    _check("sp24_gated_mxfp4", lib.sp24_gated_mxfp4(
-        m, f, k, x_codes.data_ptr(), x_scales.data_ptr(), w_codes.data_ptr(), w_scales.data_ptr(),
-        None if quantise else out.data_ptr(), out.data_ptr() if quantise else None,
-        out_scales.data_ptr() if quantise else None, _stream(dev)))
-    return (out, out_scales) if quantise else out
-
-
-def _norm_inputs(x, weight, residual, residual_out):
-    if not _is(x, _BF16, 2, None):
-        _need(x, "x", _BF16, 2)
-    m, k = x.shape
-    dev = x.device
-    if not _is(weight, _BF16, 1, dev):
-        _need(weight, "weight", _BF16, 1, dev)
-    if weight.numel() != k:
-        raise ValueError("weight must hold %d values" % k)
-    if residual is not None:
-        if not _is(residual, _BF16, 2, dev):
-            _need(residual, "residual", _BF16, 2, dev)
-        if residual.shape != x.shape:
-            raise ValueError("residual must be [%d, %d]" % (m, k))
-        residual_out = _mx4_out(residual_out, "residual_out", _BF16, (m, k), dev)
-    elif residual_out is not None:
-        raise ValueError("residual_out goes with a residual")
-    return m, k, residual_out
+    return _native.gated(x_codes, x_scales, w_codes, w_scales, quantise, out, out_scales)
 
 
 def rmsnorm(x, weight, kind=NORM_BF16, residual=None, eps=1e-6, group=128, out=None, scales=None, residual_out=None):
@@ -897,29 +813,7 @@ def rmsnorm(x, weight, kind=NORM_BF16, residual=None, eps=1e-6, group=128, out=N
     NORM_BF16 bf16 [m, k]; NORM_FP8_ROWS / NORM_INT8_ROWS codes [m, k] (uint8 or float8_e4m3fn / int8)
     and scales fp32 [m]; NORM_FP8_GROUPS scales fp32 [m, k/group]; NORM_MXFP4 codes uint8 [m, k/2] and
     scales uint8 [m * k/32] in storage order."""
-    m, k, residual_out = _norm_inputs(x, weight, residual, residual_out)
-    dev = x.device
-    if kind == NORM_MXFP4:
-        if k % 128:
-            raise ValueError("MXFP4 needs a multiple of 128 columns, got %d" % k)
-        out = _mx4_out(out, "out", _U8, (m, k // 2), dev)
-        scales = _mx4_out(scales, "scales", _U8, (m * k // 32,), dev)
-    elif kind == NORM_BF16:
-        if scales is not None:
-            raise ValueError("a bf16 output has no scales")
-        out = _mx4_out(out, "out", _BF16, (m, k), dev)
-    elif kind in (NORM_FP8_ROWS, NORM_INT8_ROWS, NORM_FP8_GROUPS):
-        if kind == NORM_FP8_GROUPS and (group < 8 or group % 8 or k % group):
-            raise ValueError("group must be a multiple of 8 that divides k=%d" % k)
-        dt = torch.int8 if kind == NORM_INT8_ROWS else _CODE_T
-        out = _mx4_out(out, "out", dt, (m, k), dev) if out is not None else torch.empty(
-            (m, k), dtype=torch.int8 if kind == NORM_INT8_ROWS else _U8, device=dev)
-        scales = _mx4_out(scales, "scales", _F32, (m, k // group) if kind == NORM_FP8_GROUPS else (m,), dev)
-    _check("sp24_rmsnorm", lib.sp24_rmsnorm(
-        kind, m, k, group, x.data_ptr(), None if residual is None else residual.data_ptr(),
-        None if residual is None else residual_out.data_ptr(), weight.data_ptr(), eps,
-        None if out is None else out.data_ptr(), None if scales is None else scales.data_ptr(), _stream(dev)))
-    return out, scales, residual_out
+    return _native.rmsnorm(x, weight, kind, residual, eps, group, out, scales, residual_out)
 
 
 def ffn_mxfp4(x, weight, gu_codes, gu_scales, down_codes, down_scales, residual=None, eps=1e-6, out=None,
@@ -928,22 +822,7 @@ def ffn_mxfp4(x, weight, gu_codes, gu_scales, down_codes, down_scales, residual=
     x (+ residual) under `weight`; gate_up W [2 f, d] (gate rows first) and down W [d, f] as MXFP4
     codes and scales.  Returns (y bf16 [m, d], residual_out or None); bit for bit rmsnorm(NORM_MXFP4),
     gated_mxfp4(quantise=True) and gemm_mxfp4 in turn."""
-    m, d, residual_out = _norm_inputs(x, weight, residual, residual_out)
-    dev = x.device
-    n2, kd = _mx4_operand(gu_codes, gu_scales, "gate_up", dev)
-    nd, f = _mx4_operand(down_codes, down_scales, "down", dev)
-    if kd != d or nd != d or n2 != 2 * f:
-        raise ValueError("gate_up must be [%d, %d] values and down [%d, %d], got [%d, %d] and [%d, %d]"
-                         % (2 * f, d, d, f, n2, kd, nd, f))
-    out = _mx4_out(out, "out", _BF16, (m, d), dev)
-    nbytes = lib.sp24_ffn_mxfp4_workspace_size(m, d, f)
-    ws = _workspace(nbytes, dev, ws)
-    _check("sp24_ffn_mxfp4", lib.sp24_ffn_mxfp4(
-        m, d, f, x.data_ptr(), None if residual is None else residual.data_ptr(),
-        None if residual is None else residual_out.data_ptr(), weight.data_ptr(), eps, gu_codes.data_ptr(),
-        gu_scales.data_ptr(), down_codes.data_ptr(), down_scales.data_ptr(), out.data_ptr(),
-        None if ws is None else ws.data_ptr(), nbytes, _stream(dev)))
-    return out, residual_out
+    return _native.ffn(x, weight, gu_codes, gu_scales, down_codes, down_scales, residual, eps, out, residual_out, ws)
 
 
 def probe_mfma_layout(variant: int, a: torch.Tensor, b: torch.Tensor, idx: torch.Tensor,

@@ -1,4 +1,4 @@
-"""Build libsp24.so (HIP, gfx950 only) in-tree.
+"""Build libsp24.so (HIP, gfx950 only) and the Python module _sp24.so in-tree.
 
     python bf16_gemm_linear_amd/build.py
 
@@ -6,7 +6,8 @@
 replaced, and fail if it predates a symbol the binding declares).
 
 Every source in csrc/ is compiled with hipcc for gfx950 and linked into
-bf16_gemm_linear_amd/libsp24.so.  No fast-math: float32 division and square
+bf16_gemm_linear_amd/libsp24.so; csrc/sp24_python.cpp, host code against PyTorch's
+headers, becomes bf16_gemm_linear_amd/_sp24.so, which loads it.  No fast-math: float32 division and square
 root stay correctly rounded (the FP8 scale and the per-value division depend on
 it), and denormals are kept.  Packed-fp32 VALU forms are switched off.
 """
@@ -23,8 +24,10 @@ CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libsp24.so")
+MODULE = os.path.join(HERE, "_sp24.so")
 
 ARCH = "gfx950"
+CXX = os.environ.get("CXX", shutil.which("g++") or "g++")
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 FLAGS = [
     "--offload-arch=" + ARCH,
@@ -55,19 +58,52 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _compile_module() -> str:
+    """The Python module's object file (host C++)."""
+    import sysconfig
+
+    from torch.utils.cpp_extension import include_paths
+    src, obj = os.path.join(CSRC, "sp24_python.cpp"), os.path.join(BUILD_DIR, "sp24_python.o")
+    inc = [os.path.join(ROOT, "include"), sysconfig.get_paths()["include"], *include_paths(),
+           os.path.join(os.path.dirname(os.path.dirname(HIPCC)), "include"), "/opt/rocm/include"]
+    cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           *("-I" + d for d in inc[:2]), *("-isystem" + d for d in inc[2:]), "-c", src, "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("%s failed for %s:\n%s" % (CXX, src, r.stderr))
+    if r.stderr.strip():
+        sys.stderr.write(r.stderr)
+    return obj
+
+
+def _link_module(obj: str) -> None:
+    import torch
+    tmp = MODULE + ".tmp"
+    cmd = [CXX, "-shared", "-o", tmp, obj, "-L" + HERE, "-l:libsp24.so", "-Wl,-rpath,$ORIGIN",
+           "-L" + os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+           "-lc10_hip"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("link failed:\n" + r.stderr)
+    os.replace(tmp, MODULE)
+
+
 def build(verbose: bool = True) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
+        module = ex.submit(_compile_module)
         objs = list(ex.map(_compile, srcs))
+        module = module.result()
     tmp = LIB + ".tmp"
     cmd = [HIPCC, "--offload-arch=" + ARCH, "-shared", "-fPIC", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("link failed:\n" + r.stderr)
     os.replace(tmp, LIB)
+    _link_module(module)
     if verbose:
-        print("built", LIB)
+        print("built", LIB, "and", os.path.basename(MODULE))
     return LIB
 
 

@@ -1,0 +1,308 @@
+// CPython binding of the MXFP4 operators and the norm: the checks of the tensors, their
+// allocation and the call in one step, since a decode step's kernels (3 to 8 us) are shorter
+// than the same checks written in Python (rmsnorm 7.7 us a call through ctypes).
+//
+// Functions take their arguments by position; None stands for an absent tensor.  Errors are
+// TypeError and ValueError for what a tensor is, and the package's error class (set_error)
+// for a status of the library.
+#define PY_SSIZE_T_CLEAN
+#include <ATen/ops/empty.h>
+#include <c10/hip/HIPStream.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include "sp24.h"
+
+namespace {
+
+using at::ScalarType;
+using at::Tensor;
+
+PyObject* g_error = nullptr;  // the package's error class: called with (function, status)
+
+struct Failed {};  // a Python error is set
+
+[[noreturn]] void fail(PyObject* type, const char* format, ...) {
+  va_list args;
+  va_start(args, format);
+  PyErr_FormatV(type, format, args);
+  va_end(args);
+  throw Failed{};
+}
+
+bool absent(PyObject* o) { return o == Py_None; }
+
+// The tensor of an argument, after the checks that every operand gets.
+const Tensor& need(PyObject* o, const char* name, std::initializer_list<ScalarType> types, int64_t ndim,
+                   const at::Device* device) {
+  if (!THPVariable_Check(o)) fail(PyExc_TypeError, "%s must be a tensor", name);
+  const Tensor& t = THPVariable_Unpack(o);
+  if (!t.is_cuda()) fail(PyExc_ValueError, "%s must be on the GPU", name);
+  if (device != nullptr && t.device() != *device)
+    fail(PyExc_ValueError, "%s is on %s, expected %s", name, t.device().str().c_str(), device->str().c_str());
+  bool known = false;
+  for (ScalarType s : types) known = known || t.scalar_type() == s;
+  if (!known)
+    fail(PyExc_TypeError, "%s has dtype %s, expected %s", name, c10::toString(t.scalar_type()),
+         c10::toString(*types.begin()));
+  if (t.dim() != ndim) fail(PyExc_ValueError, "%s must be %d-D", name, (int)ndim);
+  if (!t.is_contiguous()) fail(PyExc_ValueError, "%s must be contiguous", name);
+  return t;
+}
+
+// An output: the given tensor, of this shape, or a new one.
+Tensor output(PyObject* o, const char* name, std::initializer_list<ScalarType> types, at::IntArrayRef shape,
+              const at::Device& device) {
+  if (absent(o)) return at::empty(shape, at::TensorOptions().dtype(*types.begin()).device(device));
+  const Tensor& t = need(o, name, types, (int64_t)shape.size(), &device);
+  if (t.sizes() != shape) {
+    if (shape.size() == 1) fail(PyExc_ValueError, "%s must hold %lld values", name, (long long)shape[0]);
+    fail(PyExc_ValueError, "%s must be [%lld, %lld]", name, (long long)shape[0], (long long)shape[1]);
+  }
+  return t;
+}
+
+struct Operand {  // MXFP4: codes [rows, cols/2], scales rows * cols/32 bytes
+  const uint8_t *codes, *scales;
+  int64_t rows, cols;
+};
+Operand operand(PyObject* codes, PyObject* scales, const char* name, const at::Device* device) {
+  const Tensor& c = need(codes, name, {at::kByte}, 2, device);
+  const at::Device d = c.device();
+  const Tensor& s = need(scales, name, {at::kByte}, 1, &d);
+  const int64_t rows = c.size(0), half = c.size(1);
+  if (half % 64 != 0 || s.numel() * 16 != rows * half)
+    fail(PyExc_ValueError, "%s: codes [%lld, %lld] need a multiple of 64 columns and %lld scales, got %lld", name,
+         (long long)rows, (long long)half, (long long)(rows * half / 16), (long long)s.numel());
+  return Operand{c.const_data_ptr<uint8_t>(), s.const_data_ptr<uint8_t>(), rows, 2 * half};
+}
+
+void mx4_cols(int64_t cols) {
+  if (cols % 128 != 0) fail(PyExc_ValueError, "MXFP4 needs a multiple of 128 columns, got %lld", (long long)cols);
+}
+
+void* stream_of(const at::Device& d) { return c10::hip::getCurrentHIPStream(d.index()).stream(); }
+
+void check(const char* fn, int status) {
+  if (status == SP24_OK) return;
+  if (PyObject* e = PyObject_CallFunction(g_error, "si", fn, status)) {
+    PyErr_SetObject(g_error, e);
+    Py_DECREF(e);
+  }
+  throw Failed{};
+}
+
+// A tuple of tensors (None where undefined).
+PyObject* pack(std::initializer_list<Tensor> ts) {
+  PyObject* r = PyTuple_New((Py_ssize_t)ts.size());
+  if (r == nullptr) throw Failed{};
+  Py_ssize_t i = 0;
+  for (const Tensor& t : ts) {
+    PyObject* o = t.defined() ? THPVariable_Wrap(t) : Py_NewRef(Py_None);
+    if (o == nullptr) {
+      Py_DECREF(r);
+      throw Failed{};
+    }
+    PyTuple_SET_ITEM(r, i++, o);
+  }
+  return r;
+}
+
+int64_t integer(PyObject* o) {
+  const long long v = PyLong_AsLongLong(o);
+  if (v == -1 && PyErr_Occurred()) throw Failed{};
+  return v;
+}
+double number(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw Failed{};
+  return v;
+}
+void* data(const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
+
+PyObject* quant(PyObject* const* a) {  // x, out, scales
+  const Tensor& x = need(a[0], "x", {at::kBFloat16}, 2, nullptr);
+  const int64_t rows = x.size(0), cols = x.size(1);
+  mx4_cols(cols);
+  const at::Device d = x.device();
+  const Tensor out = output(a[1], "out", {at::kByte}, {rows, cols / 2}, d);
+  const Tensor scales = output(a[2], "scales", {at::kByte}, {rows * cols / 32}, d);
+  check("sp24_quant_mxfp4", sp24_quant_mxfp4(x.data_ptr(), rows, cols, out.data_ptr<uint8_t>(),
+                                             scales.data_ptr<uint8_t>(), stream_of(d)));
+  return pack({out, scales});
+}
+
+PyObject* dequant(PyObject* const* a) {  // codes, scales, out
+  const Operand q = operand(a[0], a[1], "operand", nullptr);
+  const at::Device d = THPVariable_Unpack(a[0]).device();
+  const Tensor out = output(a[2], "out", {at::kBFloat16}, {q.rows, q.cols}, d);
+  check("sp24_dequant_mxfp4", sp24_dequant_mxfp4(q.codes, q.scales, q.rows, q.cols, out.data_ptr(), stream_of(d)));
+  return THPVariable_Wrap(out);
+}
+
+PyObject* gemm(PyObject* const* a) {  // x codes, x scales, w codes, w scales, out
+  const Operand x = operand(a[0], a[1], "x", nullptr);
+  const at::Device d = THPVariable_Unpack(a[0]).device();
+  const Operand w = operand(a[2], a[3], "w", &d);
+  if (w.cols != x.cols)
+    fail(PyExc_ValueError, "w has %lld columns, x has %lld", (long long)w.cols, (long long)x.cols);
+  const Tensor out = output(a[4], "out", {at::kBFloat16}, {x.rows, w.rows}, d);
+  check("sp24_gemm_mxfp4", sp24_gemm_mxfp4(x.rows, w.rows, x.cols, x.codes, x.scales, w.codes, w.scales,
+                                           out.data_ptr(), stream_of(d)));
+  return THPVariable_Wrap(out);
+}
+
+PyObject* gated(PyObject* const* a) {  // x codes, x scales, w codes, w scales, quantise, out, out scales
+  const Operand x = operand(a[0], a[1], "x", nullptr);
+  const at::Device d = THPVariable_Unpack(a[0]).device();
+  const Operand w = operand(a[2], a[3], "w", &d);
+  if (w.cols != x.cols || w.rows % 2 != 0)
+    fail(PyExc_ValueError, "w must be [2 f, %lld] values, got [%lld, %lld]", (long long)x.cols, (long long)w.rows,
+         (long long)w.cols);
+  const int64_t f = w.rows / 2;
+  const int quantise = PyObject_IsTrue(a[4]);
+  if (quantise < 0) throw Failed{};
+  Tensor out, scales;
+  if (quantise) {
+    mx4_cols(f);
+    out = output(a[5], "out", {at::kByte}, {x.rows, f / 2}, d);
+    scales = output(a[6], "out_scales", {at::kByte}, {x.rows * f / 32}, d);
+  } else {
+    if (!absent(a[6])) fail(PyExc_ValueError, "out_scales goes with quantise=True");
+    out = output(a[5], "out", {at::kBFloat16}, {x.rows, f}, d);
+  }
+  check("sp24_gated_mxfp4",
+        sp24_gated_mxfp4(x.rows, f, x.cols, x.codes, x.scales, w.codes, w.scales, quantise ? nullptr : out.data_ptr(),
+                         quantise ? out.data_ptr<uint8_t>() : nullptr,
+                         quantise ? scales.data_ptr<uint8_t>() : nullptr, stream_of(d)));
+  return quantise ? pack({out, scales}) : THPVariable_Wrap(out);
+}
+
+struct NormInputs {
+  const Tensor &x, &weight;
+  Tensor residual, residual_out;
+  int64_t m, k;
+};
+NormInputs norm_inputs(PyObject* xo, PyObject* wo, PyObject* ro, PyObject* roo) {
+  const Tensor& x = need(xo, "x", {at::kBFloat16}, 2, nullptr);
+  const at::Device d = x.device();
+  const Tensor& w = need(wo, "weight", {at::kBFloat16}, 1, &d);
+  NormInputs n{x, w, Tensor(), Tensor(), x.size(0), x.size(1)};
+  if (w.numel() != n.k) fail(PyExc_ValueError, "weight must hold %lld values", (long long)n.k);
+  if (!absent(ro)) {
+    n.residual = need(ro, "residual", {at::kBFloat16}, 2, &d);
+    if (n.residual.sizes() != x.sizes())
+      fail(PyExc_ValueError, "residual must be [%lld, %lld]", (long long)n.m, (long long)n.k);
+    n.residual_out = output(roo, "residual_out", {at::kBFloat16}, {n.m, n.k}, d);
+  } else if (!absent(roo)) {
+    fail(PyExc_ValueError, "residual_out goes with a residual");
+  }
+  return n;
+}
+
+PyObject* rmsnorm(PyObject* const* a) {  // x, weight, kind, residual, eps, group, out, scales, residual_out
+  const NormInputs n = norm_inputs(a[0], a[1], a[3], a[8]);
+  const int64_t kind = integer(a[2]), group = integer(a[5]);
+  const double eps = number(a[4]);
+  const at::Device d = n.x.device();
+  Tensor out, scales;
+  switch (kind) {
+    case SP24_NORM_MXFP4:
+      mx4_cols(n.k);
+      out = output(a[6], "out", {at::kByte}, {n.m, n.k / 2}, d);
+      scales = output(a[7], "scales", {at::kByte}, {n.m * n.k / 32}, d);
+      break;
+    case SP24_NORM_BF16:
+      if (!absent(a[7])) fail(PyExc_ValueError, "a bf16 output has no scales");
+      out = output(a[6], "out", {at::kBFloat16}, {n.m, n.k}, d);
+      break;
+    case SP24_NORM_INT8_ROWS:
+      out = output(a[6], "out", {at::kChar}, {n.m, n.k}, d);
+      scales = output(a[7], "scales", {at::kFloat}, {n.m}, d);
+      break;
+    case SP24_NORM_FP8_ROWS:
+      out = output(a[6], "out", {at::kByte, at::kFloat8_e4m3fn}, {n.m, n.k}, d);
+      scales = output(a[7], "scales", {at::kFloat}, {n.m}, d);
+      break;
+    case SP24_NORM_FP8_GROUPS:
+      if (group < 8 || group % 8 != 0 || n.k % group != 0)
+        fail(PyExc_ValueError, "group must be a multiple of 8 that divides k=%lld", (long long)n.k);
+      out = output(a[6], "out", {at::kByte, at::kFloat8_e4m3fn}, {n.m, n.k}, d);
+      scales = output(a[7], "scales", {at::kFloat}, {n.m, n.k / group}, d);
+      break;
+    default: fail(PyExc_ValueError, "unknown norm kind %lld", (long long)kind);
+  }
+  check("sp24_rmsnorm", sp24_rmsnorm((int)kind, n.m, n.k, group, n.x.data_ptr(), data(n.residual),
+                                     data(n.residual_out), n.weight.data_ptr(), (float)eps, out.data_ptr(),
+                                     data(scales), stream_of(d)));
+  return pack({out, scales, n.residual_out});
+}
+
+// x, weight, gate_up codes and scales, down codes and scales, residual, eps, out, residual_out, ws
+PyObject* ffn(PyObject* const* a) {
+  const NormInputs n = norm_inputs(a[0], a[1], a[6], a[9]);
+  const at::Device d = n.x.device();
+  const Operand gu = operand(a[2], a[3], "gate_up", &d), dn = operand(a[4], a[5], "down", &d);
+  const int64_t f = dn.cols;
+  if (gu.cols != n.k || dn.rows != n.k || gu.rows != 2 * f)
+    fail(PyExc_ValueError, "gate_up must be [%lld, %lld] values and down [%lld, %lld], got [%lld, %lld] and [%lld, %lld]",
+         (long long)(2 * f), (long long)n.k, (long long)n.k, (long long)f, (long long)gu.rows, (long long)gu.cols,
+         (long long)dn.rows, (long long)f);
+  const double eps = number(a[7]);
+  const Tensor out = output(a[8], "out", {at::kBFloat16}, {n.m, n.k}, d);
+  const size_t bytes = sp24_ffn_mxfp4_workspace_size(n.m, n.k, f);
+  Tensor ws;
+  if (!absent(a[10])) {
+    if (!THPVariable_Check(a[10])) fail(PyExc_TypeError, "ws must be a tensor");
+    ws = THPVariable_Unpack(a[10]);
+    if (!ws.is_cuda() || ws.device() != d || !ws.is_contiguous())
+      fail(PyExc_ValueError, "ws must be contiguous and on %s", d.str().c_str());
+  }
+  if (bytes > 0 && (!ws.defined() || (size_t)ws.nbytes() < bytes))
+    ws = at::empty({(int64_t)bytes}, at::TensorOptions().dtype(at::kByte).device(d));
+  check("sp24_ffn_mxfp4", sp24_ffn_mxfp4(n.m, n.k, f, n.x.data_ptr(), data(n.residual), data(n.residual_out),
+                                         n.weight.data_ptr(), (float)eps, gu.codes, gu.scales, dn.codes, dn.scales,
+                                         out.data_ptr(), data(ws), bytes, stream_of(d)));
+  return pack({out, n.residual_out});
+}
+
+// No C++ exception leaves a function: what torch throws becomes a RuntimeError.
+template <PyObject* (*F)(PyObject* const*), int COUNT>
+PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t count) {
+  if (count != COUNT) {
+    PyErr_Format(PyExc_TypeError, "expected %d arguments, got %zd", COUNT, count);
+    return nullptr;
+  }
+  try {
+    return F(args);
+  } catch (const Failed&) {
+  } catch (const std::exception& e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (...) {
+    PyErr_SetString(PyExc_RuntimeError, "unknown C++ exception");
+  }
+  return nullptr;
+}
+
+PyObject* set_error(PyObject*, PyObject* cls) {
+  Py_INCREF(cls);
+  Py_XSETREF(g_error, cls);
+  Py_RETURN_NONE;
+}
+
+template <PyObject* (*F)(PyObject* const*), int COUNT>
+PyMethodDef method(const char* name) {
+  return PyMethodDef{name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<F, COUNT>)),
+                     METH_FASTCALL, nullptr};
+}
+
+PyMethodDef g_methods[] = {
+    method<quant, 3>("quant"),     method<dequant, 3>("dequant"), method<gemm, 5>("gemm"),
+    method<gated, 7>("gated"),     method<rmsnorm, 9>("rmsnorm"), method<ffn, 11>("ffn"),
+    {"set_error", set_error, METH_O, nullptr},
+    {nullptr, nullptr, 0, nullptr},
+};
+PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_sp24", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__sp24() { return PyModule_Create(&g_module); }

@@ -299,3 +299,44 @@ def test_scales_past_4gib():
     ref, mag = R.gemm_ref(x, w)
     # k = 131072: 2048 accumulations of an instruction, 8 times those ACC was derived for
     assert (np.abs(got - ref) <= 2.0 ** -8 * np.abs(ref) + 8 * ACC * mag).all()
+
+
+def test_binding_refusals():
+    """What the binding refuses on GPU tensors: types, shapes, strides, devices, outputs, sizes."""
+    sp = need_sp()
+    announce("mxfp4 binding refusals")
+    x = torch.zeros(4, 256, dtype=torch.bfloat16, device=DEV)
+    w = torch.zeros(256, dtype=torch.bfloat16, device=DEV)
+    c, s = sp.quant_mxfp4(x)
+    wide = torch.zeros(4, 512, dtype=torch.bfloat16, device=DEV)[:, :256]
+    for bad, err in ((x.float(), TypeError), (x.cpu(), ValueError), (x[0], ValueError), (wide, ValueError),
+                     (x[:, :200].contiguous(), ValueError), (x[:0], sp.Sp24Error), (None, TypeError)):
+        with pytest.raises(err):
+            sp.quant_mxfp4(bad)
+    for kw in (dict(out=c.view(8, 64)), dict(out=c.int()), dict(scales=s[:-1]), dict(out=c.cpu())):
+        with pytest.raises((ValueError, TypeError)):
+            sp.quant_mxfp4(x, **kw)
+    c2, s2 = sp.quant_mxfp4(torch.zeros(6, 384, dtype=torch.bfloat16, device=DEV))
+    for args in ((c, s, c2, s2), (c, s[:-1], c, s), (c[:, :60].contiguous(), s, c, s), (c.cpu(), s, c, s)):
+        with pytest.raises(ValueError):
+            sp.gemm_mxfp4(*args)
+    for args, kw in (((c, s, c[:3].contiguous(), s[:24].contiguous()), {}), ((c, s, c, s), dict(quantise=True)),
+                     ((c, s, c, s), dict(out_scales=s)), ((c, s, c, s), dict(out=x))):
+        with pytest.raises(ValueError):
+            sp.gated_mxfp4(*args, **kw)
+    for kw in (dict(kind=9), dict(residual=x[:2]), dict(residual_out=x), dict(kind=sp.NORM_FP8_GROUPS, group=100),
+               dict(scales=torch.zeros(4, device=DEV)), dict(kind=sp.NORM_MXFP4, out=x),
+               dict(kind=sp.NORM_FP8_ROWS, scales=torch.zeros(3, device=DEV))):
+        with pytest.raises((ValueError, TypeError)):
+            sp.rmsnorm(x, w, **kw)
+    with pytest.raises(ValueError):
+        sp.rmsnorm(x, w[:128])
+    for eps in (0.0, float("nan")):
+        with pytest.raises(sp.Sp24Error) as e:
+            sp.rmsnorm(x, w, eps=eps)
+        assert e.value.status == -7
+    with pytest.raises(sp.Sp24Error) as e:
+        sp.rmsnorm(x, w, residual=wide.contiguous(), residual_out=x)   # an output over an input
+    assert e.value.status == -8
+    with pytest.raises(ValueError):
+        sp.ffn_mxfp4(x, w, c, s, c, s)
