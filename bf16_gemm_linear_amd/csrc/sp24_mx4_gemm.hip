@@ -1,16 +1,25 @@
 // Which kernel multiplies two MXFP4 operands: the one with the least expected time (host only).
 //
 // Every kernel gives a workgroup a tile of the output and walks K in steps of 256.  Its time is
-// taken as a + r (b + c s): r rounds of workgroups over the CUs (in halves where two share a CU),
-// s steps in a row (of the K that one wave walks, where waves share K), and a, b, c of the
-// configuration, in microseconds, fitted to 3500 measured calls (m from 4 to 4096, ten (n, k) from
-// (512, 8192) to (28672, 4096), in HIP graphs; the fits' errors are 5 to 11% rms, and the calls so
-// chosen took 1.0% longer than the best configuration of each on average, 20% at most).  What the
-// numbers say: few tokens go to the stream kernel, whose waves walk K apart and pull W at the rate
-// of memory; long K over few tiles to the wave kernel (m = 256, 4096 x 14336: 16.2 us against 21 on
-// tiles); short K and many tiles to the tiled one (m = 512, 4096 x 4096: 11.4 against 12.1; m =
-// 1024, 14336 x 4096: 36.8 against 65).  Splitting K over workgroups with a reduction was measured
-// too and gained at one shape of fifty (n = 512, k = 8192): it is not built.
+// taken as
+//   a + r (b + c s) + d f s + e W + g Y,
+// r rounds of workgroups over the CUs (in halves where two share a CU) and f the same unrounded
+// (a partly filled last round costs less than a whole one: the chip clocks higher and memory is
+// freer), s steps in a row (of the K that one wave walks, where waves share K), W the megabytes of
+// the weight (memory streams them) and Y the megabytes written; the factors are each
+// configuration's, in microseconds, fitted to 29000 measured calls: 4600 shapes (m from 1 to 9000;
+// n to 30600 and k to 28672, layers' and any), up to seven configurations each, in HIP graphs.  The
+// fits' errors are 4 to 9% rms.  On 980 shapes kept out of a fit the picks took 1.6% longer than
+// the best configuration measured, 11% at the 95th percentile (of all: 1.0% from 1025 tokens, 1.3%
+// to 16, 2.8% from 65 to 256); with a, b and c alone it was 2.7%.
+// What the numbers say: few tokens go to the stream kernel, whose waves walk K apart and pull W at
+// the rate of memory; long K over few tiles to the wave kernel (m = 256, 4096 x 14336: 16.2 us
+// against 21 on tiles); short K and many tiles to the tiled one (m = 1024, 14336 x 4096: 36.8
+// against 65), on 128 x 128 tiles until rounds of 256 x 256 are many or well filled (5000 x 4096 x
+// 4096: 50.8 us against 60.9; 6000 x 8192 x 8192: 224 against 196).
+// Measured and not built: splitting K over workgroups with a reduction (gained at one shape of
+// fifty, n = 512, k = 8192), and a call's columns in two launches, whole rounds of large tiles and
+// the rest on small ones (slower or equal at 12 of 14 shapes).
 #include <stdio.h>
 #include <stdlib.h>
 #include <string.h>
@@ -32,33 +41,33 @@ struct Mx4Config {
   int log_kw;    // log2 of the waves that share K
   int min_m, max_m;
   bool gated, gated_mx4;  // can run those outputs
-  double a, b, c;
+  double a, b, c, d, e, g;
 };
 
 constexpr int kAny = 1 << 30;
 constexpr Mx4Config kConfigs[] = {
-    {STREAM, 1, 4, 4, 0, 3, 1, 16, false, false, 1.34, 1.11, 0.713},
-    {STREAM, 1, 4, 5, 0, 3, 17, 32, false, false, 1.22, 1.09, 1.092},
-    {STREAM, 1, 4, 6, 0, 2, 33, 64, false, false, 0.90, 1.89, 0.766},
-    {STREAM, 2, 5, 4, 0, 3, 1, 16, true, false, 0.93, 1.59, 1.091},
-    {STREAM, 2, 5, 5, 0, 3, 17, 32, true, false, 0.91, 1.61, 1.449},
-    {STREAM, 2, 5, 6, 0, 2, 33, 64, true, false, 0.74, 2.30, 1.077},
-    {STREAM, 4, 6, 4, 0, 2, 1, 16, true, true, -1.23, 4.51, 0.973},
-    {STREAM, 4, 6, 5, 0, 2, 17, 32, true, true, -1.54, 4.80, 1.113},
-    {STREAM, 4, 6, 6, 0, 2, 33, 64, true, true, -1.19, 4.88, 1.515},
-    {STREAM, 8, 7, 4, 0, 2, 1, 16, true, true, 1.52, 1.52, 1.631},
-    {WAVE, 0, 7, 7, 0, 2, 1, kAny, true, true, -1.03, 8.45, 1.991},
-    {WAVE, 1, 7, 6, 0, 2, 1, kAny, true, true, 0.59, 4.88, 1.366},
-    {WAVE, 2, 6, 7, 0, 2, 1, kAny, true, true, 0.19, 4.99, 1.268},
-    {WAVE, 3, 6, 6, 0, 2, 1, kAny, true, true, 1.03, 2.96, 0.821},
-    {WAVE, 4, 6, 5, 0, 2, 1, kAny, true, true, 1.53, 2.03, 0.621},
-    {WAVE, 5, 5, 6, 0, 2, 1, kAny, false, false, 1.45, 1.94, 0.575},
-    {TILED, 0, 8, 8, 0, 0, 1, kAny, true, true, -10.84, 18.95, 1.285},
-    {TILED, 1, 8, 7, 0, 0, 1, kAny, true, true, -4.08, 8.77, 0.899},
-    {TILED, 2, 7, 7, 1, 0, 1, kAny, true, true, 2.65, 1.09, 0.623},
-    {TILED, 3, 7, 6, 1, 0, 1, kAny, true, true, 3.49, 0.13, 0.453},
-    {TILED, 4, 6, 7, 1, 0, 1, kAny, false, false, 4.37, -1.04, 0.459},
-    {TILED, 5, 6, 6, 1, 0, 1, kAny, false, false, 4.19, -1.05, 0.339},
+    {STREAM, 1, 4, 4, 0, 3, 1, 16, false, false, 1.21, 1.05, 0.220, 0.142, 0.070, 5.575},
+    {STREAM, 1, 4, 5, 0, 3, 17, 32, false, false, 1.06, 0.90, 0.650, 0.153, 0.027, 3.870},
+    {STREAM, 1, 4, 6, 0, 2, 33, 64, false, false, 0.00, 2.01, 0.701, 0.000, 0.000, 3.018},
+    {STREAM, 2, 5, 4, 0, 3, 1, 16, true, false, 1.22, 1.32, 0.197, 0.236, 0.088, 2.439},
+    {STREAM, 2, 5, 5, 0, 3, 17, 32, true, false, 1.38, 1.34, 0.682, 0.000, 0.092, 0.540},
+    {STREAM, 2, 5, 6, 0, 2, 33, 64, true, false, 0.00, 2.83, 0.736, 0.000, 0.068, 1.238},
+    {STREAM, 4, 6, 4, 0, 2, 1, 16, true, true, 0.90, 1.93, 0.120, 0.198, 0.100, 1.196},
+    {STREAM, 4, 6, 5, 0, 2, 17, 32, true, true, 0.92, 1.89, 0.320, 0.307, 0.081, 1.366},
+    {STREAM, 4, 6, 6, 0, 2, 33, 64, true, true, 0.00, 3.68, 0.897, 0.000, 0.094, 0.245},
+    {STREAM, 8, 7, 4, 0, 2, 1, 16, true, true, 1.18, 2.16, 0.174, 0.371, 0.109, 0.206},
+    {WAVE, 0, 7, 7, 0, 2, 1, kAny, true, true, 0.00, 6.51, 1.605, 0.338, 0.073, 0.238},
+    {WAVE, 1, 7, 6, 0, 2, 1, kAny, true, true, 0.00, 4.21, 1.220, 0.000, 0.097, 0.362},
+    {WAVE, 2, 6, 7, 0, 2, 1, kAny, true, true, 0.25, 4.40, 1.134, 0.142, 0.063, 0.166},
+    {WAVE, 3, 6, 6, 0, 2, 1, kAny, true, true, 0.51, 2.75, 0.645, 0.000, 0.075, 0.430},
+    {WAVE, 4, 6, 5, 0, 2, 1, kAny, true, true, 0.66, 2.10, 0.446, 0.000, 0.095, 0.447},
+    {WAVE, 5, 5, 6, 0, 2, 1, kAny, false, false, 1.45, 1.25, 0.478, 0.000, 0.059, 0.958},
+    {TILED, 0, 8, 8, 0, 0, 1, kAny, true, true, 0.00, 6.30, 1.565, 0.000, 0.054, 0.106},
+    {TILED, 1, 8, 7, 0, 0, 1, kAny, true, true, 0.00, 2.50, 1.095, 0.030, 0.068, 0.173},
+    {TILED, 2, 7, 7, 1, 0, 1, kAny, true, true, 2.92, 0.66, 0.247, 0.359, 0.059, 0.049},
+    {TILED, 3, 7, 6, 1, 0, 1, kAny, true, true, 2.38, 0.87, 0.387, 0.008, 0.057, 0.002},
+    {TILED, 4, 6, 7, 1, 0, 1, kAny, false, false, 3.36, 0.00, 0.269, 0.141, 0.030, 0.154},
+    {TILED, 5, 6, 6, 1, 0, 1, kAny, false, false, 2.99, 0.00, 0.145, 0.134, 0.039, 0.159},
 };
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -86,12 +95,15 @@ const Mx4Config& plan(const Mx4Args& a) {
   const Mx4Config* best = nullptr;
   double least = 0;
   const int64_t steps = ceil_shift(a.k, kLogStep);
+  const double weight = (a.gated ? 2e-6 : 1e-6) * 0.53 * (double)a.n * a.k, written = 2e-6 * (double)a.m * a.n;
   for (const Mx4Config& c : kConfigs) {
     if (a.m < c.min_m || a.m > c.max_m || (a.gated && !(a.hq != nullptr ? c.gated_mx4 : c.gated))) continue;
     const int64_t tiles = ceil_shift(a.n, a.gated ? c.log_n - 1 : c.log_n) * ceil_shift(a.m, c.log_m);
     const int64_t parts = ceil_shift(tiles << c.log_share, kLogCus);  // rounds, in 1 / share
     const double rounds = parts <= 1 << c.log_share ? 1.0 : (double)parts / (1 << c.log_share);
-    const double t = c.a + rounds * (c.b + c.c * (double)ceil_shift(steps, c.log_kw));
+    const double s = (double)ceil_shift(steps, c.log_kw);
+    const double filled = tiles <= kCus ? 1.0 : (double)tiles / kCus;
+    const double t = c.a + rounds * (c.b + c.c * s) + c.d * filled * s + c.e * weight + c.g * written;
     if (best == nullptr || t < least) {
       best = &c;
       least = t;
