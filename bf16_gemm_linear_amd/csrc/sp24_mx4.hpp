@@ -63,20 +63,48 @@ __device__ __forceinline__ uint32_t mx4_codes8(const float* v, uint32_t byte) {
   return byte == 255u ? 0u : q;
 }
 
+// One step of a butterfly over lanes: f(v, the value of the lanes OFF away), where aligned groups
+// of OFF lanes hold the same value already (steps 1, 2, 4, ... in turn).  Register exchanges
+// throughout, a few cycles each; through LDS (a shuffle) a step takes about a hundred.
+template <int OFF, class F>
+__device__ __forceinline__ uint32_t fold_lanes(uint32_t v, F f) {
+  if constexpr (OFF == 32) {
+    const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return f((uint32_t)r[0], (uint32_t)r[1]);
+  } else if constexpr (OFF == 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return f((uint32_t)r[0], (uint32_t)r[1]);
+  } else {  // within 16 lanes: swaps in a quad, a half row mirrored, a row mirrored
+    constexpr int CTRL = OFF == 1 ? 0xB1 : OFF == 2 ? 0x4E : OFF == 4 ? 0x141 : 0x140;
+    return f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true));
+  }
+}
+__device__ __forceinline__ uint32_t bits_max(uint32_t a, uint32_t b) { return max(a, b); }
+__device__ __forceinline__ uint32_t bits_or(uint32_t a, uint32_t b) { return a | b; }
+__device__ __forceinline__ uint32_t bits_sum(uint32_t a, uint32_t b) {
+  return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+}
+template <class F>
+__device__ __forceinline__ uint32_t fold_wave(uint32_t v, F f) {
+  v = fold_lanes<1>(v, f);
+  v = fold_lanes<2>(v, f);
+  v = fold_lanes<4>(v, f);
+  v = fold_lanes<8>(v, f);
+  v = fold_lanes<16>(v, f);
+  return fold_lanes<32>(v, f);
+}
+
 // The scale byte of each 32-value block held by 4 neighbouring lanes (8 values a
 // lane), from each lane's largest magnitude `key` (bits of a bf16 with SHIFT 7,
 // of a float with SHIFT 23, sign cleared); and the word of the 4 blocks of 16 lanes.
 template <int SHIFT>
 __device__ __forceinline__ uint32_t mx4_block_byte(uint32_t key) {
-  key = max(key, (uint32_t)__shfl_xor((int)key, 1, 64));
-  key = max(key, (uint32_t)__shfl_xor((int)key, 2, 64));
+  key = fold_lanes<2>(fold_lanes<1>(key, bits_max), bits_max);
   return mx4_scale_byte(key >> SHIFT, key == 0);
 }
 __device__ __forceinline__ uint32_t mx4_word_of_blocks(uint32_t byte, int lane) {
-  uint32_t w = byte << (8 * ((lane >> 2) & 3));
-  w |= (uint32_t)__shfl_xor((int)w, 4, 64);
-  w |= (uint32_t)__shfl_xor((int)w, 8, 64);
-  return w;
+  const uint32_t w = byte << (8 * ((lane >> 2) & 3));
+  return fold_lanes<8>(fold_lanes<4>(w, bits_or), bits_or);
 }
 
 // Two floats -> two bf16, nearest even, NaN kept a NaN.

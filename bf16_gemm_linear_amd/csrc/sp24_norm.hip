@@ -3,10 +3,11 @@
 // v = t rstd w with rstd = 1 / sqrt(mean(t^2) + eps).
 //
 // Memory-bound: 2 bytes read a value (6 moved with a residual) and 1 written (E4M3, INT8).
-// 8191 x 8192 with a residual to E4M3 takes 82 us with a scale per group of 128, 5.7 TB/s
-// (a large copy: 5.1), and 68 with a scale per row when its inputs stay in the last-level
-// cache (89 without the outputs' non-temporal hint, which makes no difference for 16 rows).
-// 1 x 4096 takes 3.0 us, the time of a launch and two trips to memory.
+// 8191 x 8192 with a residual takes 81 us to E4M3 with a scale per row, 83 with one per group
+// of 128 and 77 to MXFP4, 5.7 TB/s (a large copy: 5.1); the outputs' non-temporal hint is worth
+// a quarter of it where the inputs come from the last-level cache (68 us, 89 without).  Few rows
+// are bound by a thread's chain of instructions: reductions over lanes go by register exchanges
+// (through LDS: 1 x 4096 to E4M3 3.1 us, per group 4.1; now 2.5 and 2.6, 1.7 any launch's).
 // One pass: a row stays in registers as fp32 from the loads to the codes, T threads a row
 // with NV vectors of 8 values each.  The codes do not wait for rstd: with u = t w, a scale
 // is s = max|u| rstd / top, so v / s = u (top / max|u|), and one reduction over the row
@@ -57,15 +58,15 @@ __device__ __forceinline__ u32x2 norm_codes8(const float* u, const NormDiv& d) {
   }
 }
 
-// T threads a row (64: one wave, four rows a workgroup), NV vectors of 8 values a thread.
+// T threads a row (64: one wave, four rows a workgroup; 128: two rows), NV vectors of 8 values a thread.
 // Groups (SP24_NORM_FP8_GROUPS): segments of `seg` lanes, seg a power of two dividing the
 // group's vectors; where a group is more than one segment its maximum is collected in LDS
 // (integer maxima: the order does not matter).
 template <int KIND, int T, int NV>
 __global__ __launch_bounds__(T < 256 ? 256 : T) void rmsnorm_kernel(
     const uint16_t* __restrict__ x, const uint16_t* residual, uint16_t* residual_out,
-    const uint16_t* __restrict__ w, int64_t m, int k, float eps, int group, int seg, void* __restrict__ out,
-    void* __restrict__ scales) {
+    const uint16_t* __restrict__ w, int64_t m, int k, float eps, int group, int seg, int ng,
+    uint32_t per_group, void* __restrict__ out, void* __restrict__ scales) {
   constexpr int RPB = T < 256 ? 256 / T : 1, NW = T / 64;
   constexpr bool GROUPS = KIND == SP24_NORM_FP8_GROUPS;
   __shared__ float sh_sum[RPB * NW];
@@ -76,66 +77,80 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rmsnorm_kernel(
   const int64_t row = (int64_t)blockIdx.x * RPB + rl;
   const int nv = row < m ? k / 8 : 0;
   const size_t base = (size_t)row * (k / 8);
-  const int vpg = GROUPS ? group / 8 : 1, ng = GROUPS ? k / group : 1;
+  const int vpg = GROUPS ? group / 8 : 1;
+  // vector i's group: i / vpg by the factor ceil(2^31 / vpg), exact for i and vpg to 2^13
+  auto group_of = [&](int i) { return (int)__umulhi(2u * (uint32_t)i, per_group); };
   const bool in_lds = GROUPS && vpg != seg;
   if (in_lds) {
     for (int i = threadIdx.x; i < RPB * ng; i += (T < 256 ? 256 : T)) gmax[i] = 0;
     __syncthreads();
   }
 
-  u32x4 xd[NV], rd[NV], wd[NV];
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int i = tl + j * T;
-    xd[j] = rd[j] = wd[j] = u32x4{0u, 0u, 0u, 0u};
-    if (i < nv) {
-      xd[j] = reinterpret_cast<const u32x4*>(x)[base + i];
-      if (residual != nullptr) rd[j] = reinterpret_cast<const u32x4*>(residual)[base + i];
-      wd[j] = reinterpret_cast<const u32x4*>(w)[i];
-    }
-  }
+  // vectors are loaded B at a time: all of a long row's at once would not fit in the registers
+  // beside u (1024 x 65536 to E4M3: 134 us, in pairs 43)
+  constexpr int B = NV > 4 ? 2 : NV;
+  constexpr bool KEEP_W = KIND == SP24_NORM_BF16 && NV <= 4;  // the weight for the output (longer rows load it again)
+  u32x4 wd[KEEP_W ? NV : B];
   float u[NV][8], ss = 0.0f;
   uint32_t key = 0, gkey[NV];
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int i = tl + j * T;
-    uint32_t mk = 0;
+  for (int j0 = 0; j0 < NV; j0 += B) {
+    u32x4 xd[B], rd[B];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint32_t xe = (e & 1) ? xd[j][e / 2] & 0xFFFF0000u : xd[j][e / 2] << 16;
-      const uint32_t re = (e & 1) ? rd[j][e / 2] & 0xFFFF0000u : rd[j][e / 2] << 16;
-      float t = __uint_as_float(xe);
-      if (residual != nullptr) t += __uint_as_float(re);
-      ss = __builtin_fmaf(t, t, ss);
-      u[j][e] = t;
-    }
-    if (residual != nullptr && i < nv) {
-      const u32x4 o{f32x2_to_bf16x2(u[j][0], u[j][1]), f32x2_to_bf16x2(u[j][2], u[j][3]),
-                    f32x2_to_bf16x2(u[j][4], u[j][5]), f32x2_to_bf16x2(u[j][6], u[j][7])};
-      __builtin_nontemporal_store(o, reinterpret_cast<u32x4*>(residual_out) + base + i);
+    for (int b = 0; b < B; ++b) {
+      const int i = tl + (j0 + b) * T;
+      xd[b] = rd[b] = wd[b] = u32x4{0u, 0u, 0u, 0u};
+      if (i < nv) {
+        xd[b] = reinterpret_cast<const u32x4*>(x)[base + i];
+        if (residual != nullptr) rd[b] = reinterpret_cast<const u32x4*>(residual)[base + i];
+        wd[b] = reinterpret_cast<const u32x4*>(w)[i];
+      }
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint32_t we = (e & 1) ? wd[j][e / 2] & 0xFFFF0000u : wd[j][e / 2] << 16;
-      // bf16 output keeps t (v = t rstd w, as the formula reads); the others u = t w
-      if constexpr (KIND != SP24_NORM_BF16) u[j][e] *= __uint_as_float(we);
-      mk = max(mk, __float_as_uint(u[j][e]) & 0x7FFFFFFFu);
-    }
-    key = max(key, mk);
-    if constexpr (GROUPS) {
+    for (int b = 0; b < B; ++b) {
+      const int j = j0 + b, i = tl + j * T;
+      uint32_t mk = 0;
 #pragma unroll
-      for (int off = 1; off < 64; off <<= 1)  // unrolled: constant distances need no address
-        if (off < seg) mk = max(mk, (uint32_t)__shfl_xor((int)mk, off, 64));
-      gkey[j] = mk;
-      if (in_lds && i < nv && lane % seg == 0) atomicMax(&gmax[rl * ng + i / vpg], mk);
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t xe = (e & 1) ? xd[b][e / 2] & 0xFFFF0000u : xd[b][e / 2] << 16;
+        const uint32_t re = (e & 1) ? rd[b][e / 2] & 0xFFFF0000u : rd[b][e / 2] << 16;
+        float t = __uint_as_float(xe);
+        if (residual != nullptr) t += __uint_as_float(re);
+        ss = __builtin_fmaf(t, t, ss);
+        u[j][e] = t;
+      }
+      if (residual != nullptr && i < nv) {
+        const u32x4 o{f32x2_to_bf16x2(u[j][0], u[j][1]), f32x2_to_bf16x2(u[j][2], u[j][3]),
+                      f32x2_to_bf16x2(u[j][4], u[j][5]), f32x2_to_bf16x2(u[j][6], u[j][7])};
+        __builtin_nontemporal_store(o, reinterpret_cast<u32x4*>(residual_out) + base + i);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t we = (e & 1) ? wd[b][e / 2] & 0xFFFF0000u : wd[b][e / 2] << 16;
+        // bf16 output keeps t (v = t rstd w, as the formula reads); the others u = t w
+        if constexpr (KIND != SP24_NORM_BF16) u[j][e] *= __uint_as_float(we);
+        mk = max(mk, __float_as_uint(u[j][e]) & 0x7FFFFFFFu);
+      }
+      key = max(key, mk);
+      if constexpr (GROUPS) {
+        if (seg > 1) mk = fold_lanes<1>(mk, bits_max);
+        if (seg > 2) mk = fold_lanes<2>(mk, bits_max);
+        if (seg > 4) mk = fold_lanes<4>(mk, bits_max);
+        if (seg > 8) mk = fold_lanes<8>(mk, bits_max);
+        if (seg > 16) mk = fold_lanes<16>(mk, bits_max);
+        if (seg > 32) mk = fold_lanes<32>(mk, bits_max);
+        gkey[j] = mk;
+        if (in_lds && i < nv && lane % seg == 0) atomicMax(&gmax[rl * ng + group_of(i)], mk);
+      }
+    }
+    if constexpr (B < NV) {  // finish this batch: its maximum now, not at the end
+      asm volatile("" : "+v"(key), "+v"(ss));
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
 
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) {
-    ss += __shfl_xor(ss, off, 64);
-    if constexpr (!GROUPS) key = max(key, (uint32_t)__shfl_xor((int)key, off, 64));
-  }
+  ss = __uint_as_float(fold_wave(__float_as_uint(ss), bits_sum));
+  if constexpr (!GROUPS) key = fold_wave(key, bits_max);
   if constexpr (NW > 1) {
     if (lane == 0) {
       sh_sum[threadIdx.x / 64] = ss;
@@ -146,8 +161,8 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rmsnorm_kernel(
     key = 0;
 #pragma unroll
     for (int i = 0; i < NW; ++i) {
-      ss += sh_sum[i];
-      key = max(key, sh_max[i]);
+      ss += sh_sum[rl * NW + i];
+      key = max(key, sh_max[rl * NW + i]);
     }
   } else {
     if (in_lds) __syncthreads();
@@ -164,11 +179,12 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rmsnorm_kernel(
     const int i = tl + j * T;
     if constexpr (KIND == SP24_NORM_BF16) {
       if (i < nv) {
+        const u32x4 wj = KEEP_W ? wd[KEEP_W ? j : 0] : reinterpret_cast<const u32x4*>(w)[i];
         u32x4 o;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          o[e] = f32x2_to_bf16x2(u[j][2 * e] * rstd * __uint_as_float(wd[j][e] << 16),
-                                 u[j][2 * e + 1] * rstd * __uint_as_float(wd[j][e] & 0xFFFF0000u));
+          o[e] = f32x2_to_bf16x2(u[j][2 * e] * rstd * __uint_as_float(wj[e] << 16),
+                                 u[j][2 * e + 1] * rstd * __uint_as_float(wj[e] & 0xFFFF0000u));
         __builtin_nontemporal_store(o, static_cast<u32x4*>(out) + base + i);
       }
     } else if constexpr (KIND == SP24_NORM_MXFP4) {
@@ -187,13 +203,14 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rmsnorm_kernel(
     } else {
       if (i < nv) {
         if constexpr (GROUPS) {
-          const int g = i / vpg;
+          const int g = group_of(i);
           const float s = norm_scale<KIND>(in_lds ? gmax[rl * ng + g] : gkey[j], rstd, d);
-          if (i % vpg == 0) static_cast<float*>(scales)[(size_t)row * ng + g] = s;
+          if (i == g * vpg) static_cast<float*>(scales)[(size_t)row * ng + g] = s;
         }
         __builtin_nontemporal_store(norm_codes8<KIND>(u[j], d), static_cast<u32x2*>(out) + base + i);
       }
     }
+    if constexpr (B < NV) __builtin_amdgcn_sched_barrier(0);
   }
 }
 
@@ -202,29 +219,38 @@ hipError_t launch_norm_tn(const NormArgs& a, hipStream_t s) {
   constexpr int RPB = T < 256 ? 256 / T : 1;
   int seg = 1;
   size_t lds = 0;
+  const uint64_t vpg = (uint64_t)a.group / 8;  // (any k % 8 == 0: one group a row but for SP24_NORM_FP8_GROUPS)
   if (KIND == SP24_NORM_FP8_GROUPS) {
-    const int64_t vpg = a.group / 8;
     while (seg < 64 && vpg % (2 * seg) == 0) seg *= 2;
     if (vpg != seg) lds = (size_t)RPB * (a.k / a.group) * 4;
   }
   hipLaunchKernelGGL((rmsnorm_kernel<KIND, T, NV>), dim3((uint32_t)((a.m + RPB - 1) / RPB)),
                      dim3(T < 256 ? 256 : T), lds, s, a.x, a.residual, a.residual_out, a.weight, a.m, (int)a.k,
-                     a.eps, (int)a.group, seg, a.out, a.scales);
+                     a.eps, (int)a.group, seg, (int)(a.k / a.group),
+                     (uint32_t)((((uint64_t)1 << 31) + vpg - 1) / vpg), a.out, a.scales);
   return hipGetLastError();
 }
 
-// Threads a row by its length: a wave up to 2048 values, then one workgroup with two vectors a
-// thread, which measured best (E4M3 per group of 128 and residual, us: 8191 x 8192 on 256 x 4,
-// 512 x 2 and 1024 x 1 75.5, 73.3 and 77.4; 4095 x 14336 on 512 x 4 and 1024 x 2 71.5 and 64.9;
-// one row of 8192 6.6, 5.3 and 5.2).
+// Threads a row: one vector a thread for short and few rows (to 4096 values, 2^21 in all), where
+// the chain of a thread is the time (E4M3, no residual, us: 16 x 2048 on 256 x 1 and 64 x 4 2.4 and
+// 3.2, 256 x 4096 on 512 x 1 and 256 x 2 2.8 and 3.1; with more rows it turns round, 1000 x 4096 5.3
+// and 5.0, 8191 x 4096 23.5 and 19.5).  Else a wave to 2048 values, then one workgroup with two
+// vectors a thread (8191 x 8192 E4M3 per group of 128 and residual on 512 x 2 83, on 1024 x 1 85;
+// 16 rows of 8192 3.3 and 3.5), four to 32768 (2048 x 20480 38, on 1024 x 8 51) and eight beyond.
 template <int KIND>
 hipError_t launch_norm_kind(const NormArgs& a, hipStream_t s) {
   const int64_t nv = a.k / 8;
   if (nv <= 64) return launch_norm_tn<KIND, 64, 1>(a, s);
+  if (nv <= 512 && a.m * a.k <= 1 << 21) {
+    if (nv <= 128) return launch_norm_tn<KIND, 128, 1>(a, s);
+    if (nv <= 256) return launch_norm_tn<KIND, 256, 1>(a, s);
+    return launch_norm_tn<KIND, 512, 1>(a, s);
+  }
   if (nv <= 256) return launch_norm_tn<KIND, 64, 4>(a, s);
   if (nv <= 512) return launch_norm_tn<KIND, 256, 2>(a, s);
   if (nv <= 1024) return launch_norm_tn<KIND, 512, 2>(a, s);
   if (nv <= 2048) return launch_norm_tn<KIND, 1024, 2>(a, s);
+  if (nv <= 4096) return launch_norm_tn<KIND, 1024, 4>(a, s);
   return launch_norm_tn<KIND, 1024, 8>(a, s);
 }
 

@@ -109,6 +109,37 @@ def test_mxfp4(k):
         check_mx4_output(o, s, v, REL * np.abs(v), (m, k))
 
 
+# above 2^21 values short rows take several vectors a thread (below, one: the tests above), whose
+# rows and groups end inside a thread's vectors; a part of the rows is compared
+@pytest.mark.parametrize("m,k,group", [(2101, 1000, 200), (2049, 1024, 128), (1281, 1664, 104), (1050, 2048, 8),
+                                       (1031, 2040, 408), (1000, 2176, 128), (523, 4096, 512), (600, 3648, 24)])
+def test_short_rows_in_number(m, k, group):
+    sp = need_sp()
+    assert m * k > 1 << 21
+    x, r, w = inputs(m, k, m + k, True)
+    xd, rd, wd = x.to(DEV), r.to(DEV), w.to(DEV)
+    pick = np.r_[0:3, m // 2 - 2 : m // 2 + 3, m - 4 : m]
+    v, t = R.norm_ref(W.bf16_bits(x[pick]), W.bf16_bits(r[pick]), W.bf16_bits(w), 1e-5)
+    for kind in (sp.NORM_BF16, sp.NORM_FP8_ROWS, sp.NORM_INT8_ROWS, sp.NORM_FP8_GROUPS, sp.NORM_MXFP4):
+        if kind == sp.NORM_MXFP4 and k % 128:
+            continue
+        announce("rmsnorm kind", kind, m, k, group)
+        o, s, ro = sp.rmsnorm(xd, wd, kind, residual=rd, eps=1e-5, group=group)
+        torch.cuda.synchronize()
+        assert np.array_equal(bits(ro), W.bf16_bits((x.float() + r.float()).to(torch.bfloat16)))
+        if kind == sp.NORM_BF16:
+            assert (np.abs(O.bf16_to_f64(bits(o)[pick]) - v) <= (2.0 ** -8 + REL) * np.abs(v)).all()
+        elif kind == sp.NORM_MXFP4:
+            part = torch.from_numpy(R.store_scales(R.load_scales(np8(s), m, k)[pick]))
+            check_mx4_output(o[torch.from_numpy(pick).to(DEV)], part, v, REL * np.abs(v), (m, k))
+        else:
+            q = o.float() if kind == sp.NORM_INT8_ROWS else o.view(torch.float8_e4m3fn).float()
+            q, s = q.cpu().double().numpy()[pick], s.cpu().numpy().astype(np.float64)[pick]
+            g = k // group if kind == sp.NORM_FP8_GROUPS else 1
+            check_codes(q.reshape(-1, k // g), s.reshape(-1), v.reshape(-1, k // g),
+                        127.0 if kind == sp.NORM_INT8_ROWS else 448.0, kind == sp.NORM_INT8_ROWS)
+
+
 def test_residual_in_place_and_many_rows():
     sp = need_sp()
     for m, k in ((4099, 128), (1031, 4096)):
