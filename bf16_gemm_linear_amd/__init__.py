@@ -783,46 +783,13 @@ def mxfp4_scale_index(rows: int, cols: int, device=None) -> torch.Tensor:
     return 4 * (4 * rows * (w // 4) + r * width + w % 4) + b % 4
 
 
-def quant_mxfp4(x: torch.Tensor, out: torch.Tensor | None = None, scales: torch.Tensor | None = None):
-    """bf16 [rows, cols] (cols % 128 == 0) -> MXFP4 (codes uint8 [rows, cols/2], scales uint8
-    [rows * cols/32] in storage order, see mxfp4_scale_index)."""
-    return _native.quant(x, out, scales)
-
-
-def dequant_mxfp4(codes: torch.Tensor, scales: torch.Tensor, out: torch.Tensor | None = None):
-    """The bf16 values [rows, cols] that MXFP4 codes and scales stand for (exact)."""
-    return _native.dequant(codes, scales, out)
-
-
-def gemm_mxfp4(x_codes, x_scales, w_codes, w_scales, out=None):
-    """Y = X . W^T of MXFP4 operands X [m, k] and W [n, k] (codes and scales of each); bf16 [m, n]."""
-    return _native.gemm(x_codes, x_scales, w_codes, w_scales, out)
-
-
-def gated_mxfp4(x_codes, x_scales, w_codes, w_scales, quantise=False, out=None, out_scales=None):
-    """silu(X Wg^T) * (X Wu^T) of MXFP4 operands, W = [f gate rows; f up rows]: bf16 [m, f], or with
-    quantise=True (f % 128 == 0) MXFP4 (codes, scales), the X of the next gemm_mxfp4."""
-    return _native.gated(x_codes, x_scales, w_codes, w_scales, quantise, out, out_scales)
-
-
-def rmsnorm(x, weight, kind=NORM_BF16, residual=None, eps=1e-6, group=128, out=None, scales=None, residual_out=None):
-    """RMS norm of the rows of x (+ residual) in the form the next product reads: (out, scales,
-    residual_out), scales None for NORM_BF16 and residual_out (bf16 of x + residual; may be `residual`
-    itself) None without a residual.
-
-    NORM_BF16 bf16 [m, k]; NORM_FP8_ROWS / NORM_INT8_ROWS codes [m, k] (uint8 or float8_e4m3fn / int8)
-    and scales fp32 [m]; NORM_FP8_GROUPS scales fp32 [m, k/group]; NORM_MXFP4 codes uint8 [m, k/2] and
-    scales uint8 [m * k/32] in storage order."""
-    return _native.rmsnorm(x, weight, kind, residual, eps, group, out, scales, residual_out)
-
-
-def ffn_mxfp4(x, weight, gu_codes, gu_scales, down_codes, down_scales, residual=None, eps=1e-6, out=None,
-              residual_out=None, ws=None):
-    """A pre-norm feed-forward block in MXFP4: y = down(silu(gate(v)) * up(v)), v the RMS norm of
-    x (+ residual) under `weight`; gate_up W [2 f, d] (gate rows first) and down W [d, f] as MXFP4
-    codes and scales.  Returns (y bf16 [m, d], residual_out or None); bit for bit rmsnorm(NORM_MXFP4),
-    gated_mxfp4(quantise=True) and gemm_mxfp4 in turn."""
-    return _native.ffn(x, weight, gu_codes, gu_scales, down_codes, down_scales, residual, eps, out, residual_out, ws)
+# the MXFP4 operators and the norm, as the C++ module has them (help() shows their arguments)
+quant_mxfp4 = _native.quant_mxfp4
+dequant_mxfp4 = _native.dequant_mxfp4
+gemm_mxfp4 = _native.gemm_mxfp4
+gated_mxfp4 = _native.gated_mxfp4
+rmsnorm = _native.rmsnorm
+ffn_mxfp4 = _native.ffn_mxfp4
 
 
 def probe_mfma_layout(variant: int, a: torch.Tensor, b: torch.Tensor, idx: torch.Tensor,

@@ -63,8 +63,8 @@ __device__ __forceinline__ uint32_t mx4_codes8(const float* v, uint32_t byte) {
   return byte == 255u ? 0u : q;
 }
 
-// One step of a butterfly over lanes: f(v, the value of the lanes OFF away), where aligned groups
-// of OFF lanes hold the same value already (steps 1, 2, 4, ... in turn).  Register exchanges
+// One step of a butterfly over lanes: f(v, the value of the lane OFF away); for OFF 4 and 8 aligned
+// groups of OFF lanes hold one value already (steps 1, 2, 4, ... in turn).  Register exchanges
 // throughout, a few cycles each; through LDS (a shuffle) a step takes about a hundred.
 template <int OFF, class F>
 __device__ __forceinline__ uint32_t fold_lanes(uint32_t v, F f) {

@@ -72,16 +72,16 @@ constexpr uint32_t kQuantBlocks = 8192, kDequantBlocks = 1u << 22;
 hipError_t launch_quant_mxfp4(const uint16_t* x, int64_t rows, int64_t cols, uint8_t* codes, uint32_t* scales,
                               hipStream_t s) {
   const uint32_t words = (uint32_t)(cols / 128), units = (uint32_t)(rows * words);
-  hipLaunchKernelGGL(mx4_quant_kernel, dim3(blocks_for(units, kQuantBlocks)), dim3(kThreads), 0, s, x, units, words, rows, cols,
-                     codes, scales);
+  hipLaunchKernelGGL(mx4_quant_kernel, dim3(blocks_for(units, kQuantBlocks)), dim3(kThreads), 0, s, x, units, words,
+                     rows, cols, codes, scales);
   return hipGetLastError();
 }
 
 hipError_t launch_dequant_mxfp4(const uint8_t* codes, const uint32_t* scales, int64_t rows, int64_t cols,
                                 uint16_t* out, hipStream_t s) {
   const uint32_t words = (uint32_t)(cols / 128), units = (uint32_t)(rows * words);
-  hipLaunchKernelGGL(mx4_dequant_kernel, dim3(blocks_for(units, kDequantBlocks)), dim3(kThreads), 0, s, codes, scales, units, words,
-                     rows, cols, out);
+  hipLaunchKernelGGL(mx4_dequant_kernel, dim3(blocks_for(units, kDequantBlocks)), dim3(kThreads), 0, s, codes, scales,
+                     units, words, rows, cols, out);
   return hipGetLastError();
 }
 

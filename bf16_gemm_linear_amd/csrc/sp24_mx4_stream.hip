@@ -186,8 +186,7 @@ __global__ __launch_bounds__(C::KW * 64, C::KW / 4) void mx4_stream_kernel(Mx4Ar
       uint32_t key = 0;
 #pragma unroll
       for (int e = 0; e < 8; ++e) key = max(key, __float_as_uint(v[e]) & 0x7FFFFFFFu);
-      key = max(key, (uint32_t)__shfl_xor((int)key, 16, 64));
-      key = max(key, (uint32_t)__shfl_xor((int)key, 32, 64));
+      key = fold_lanes<32>(fold_lanes<16>(key, bits_max), bits_max);
       const uint32_t byte = mx4_scale_byte(key >> 23, key == 0), c8 = mx4_codes8(v, byte);
       const int m = m0 + 16 * j + (l & 15), n = n0 + 32 * blk, qq = l >> 4;
       if (m >= p.m || 32 * blk >= nrows) continue;  // rows past the range are the next workgroup's

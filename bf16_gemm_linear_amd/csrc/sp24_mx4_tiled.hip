@@ -405,7 +405,7 @@ __global__ __launch_bounds__(C::NT, C::OCC) void mx4_tiled_kernel(Mx4Args p) {
         uint32_t key = 0;
 #pragma unroll
         for (int e = 0; e < 16; ++e) key = max(key, __float_as_uint(v[e]) & 0x7FFFFFFFu);
-        key = max(key, (uint32_t)__shfl_xor((int)key, 32, 64));
+        key = fold_lanes<32>(key, bits_max);
         const uint32_t byte = mx4_scale_byte(key >> 23, key == 0);
         const uint32_t q0 = mx4_codes8(v, byte), q1 = mx4_codes8(v + 8, byte);
         uint16_t* o = reinterpret_cast<uint16_t*>(lds + ml * ROWS + nl / 2) + h;

@@ -268,7 +268,7 @@ __global__ __launch_bounds__(C::KW * 64, C::KW / 4) void mx4_wave_kernel(Mx4Args
         uint32_t key = 0;
 #pragma unroll
         for (int e = 0; e < 16; ++e) key = max(key, __float_as_uint(v[e]) & 0x7FFFFFFFu);
-        key = max(key, (uint32_t)__shfl_xor((int)key, 32, 64));
+        key = fold_lanes<32>(key, bits_max);
         const uint32_t byte = mx4_scale_byte(key >> 23, key == 0);
         const uint32_t q0 = mx4_codes8(v, byte), q1 = mx4_codes8(v + 8, byte);
         const int nb = n0 + 32 * i;
