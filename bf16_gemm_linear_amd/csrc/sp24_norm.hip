@@ -12,7 +12,11 @@
 // with NV vectors of 8 values each.  The codes do not wait for rstd: with u = t w, a scale
 // is s = max|u| rstd / top, so v / s = u (top / max|u|), and one reduction over the row
 // gives sum t^2 and max|u| together (for groups, the maxima are taken by shuffles at the
-// same time).  Sums are fp32 in a fixed order.
+// same time).  Where a maximum of |u| has left fp32's range, or comes so near its lower end
+// that values would lose bits (very large or small weights), v itself may be in range: such a
+// row takes the maxima of |t rstd w| in a second reduction.  For that t stays in the registers,
+// and t w is formed twice: 1 to 4% of a call to 32768 values, 11% beyond, where the weight is
+// loaded again (1024 x 65536 to E4M3 49 us from 44).  Sums are fp32 in a fixed order.
 #include "sp24_fp8.hpp"
 #include "sp24_mx4.hpp"
 
@@ -58,6 +62,15 @@ __device__ __forceinline__ u32x2 norm_codes8(const float* u, const NormDiv& d) {
   }
 }
 
+// Value e of a vector of 8 bf16.
+__device__ __forceinline__ float bf16_of(const u32x4& d, int e) {
+  return __uint_as_float((e & 1) ? d[e / 2] & 0xFFFF0000u : d[e / 2] << 16);
+}
+
+// Whether products u = t w with this largest magnitude (bits) may not stand for v: it is Inf or
+// NaN, or below 2^-100, where a product under 2^-126 (fewer bits) still counts beside it.
+__device__ __forceinline__ bool out_of_range(uint32_t key) { return key >= 0x7F800000u || key < 0x0D800000u; }
+
 // T threads a row (64: one wave, four rows a workgroup; 128: two rows), NV vectors of 8 values a thread.
 // Groups (SP24_NORM_FP8_GROUPS): segments of `seg` lanes, seg a power of two dividing the
 // group's vectors; where a group is more than one segment its maximum is collected in LDS
@@ -69,8 +82,9 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rmsnorm_kernel(
     uint32_t per_group, void* __restrict__ out, void* __restrict__ scales) {
   constexpr int RPB = T < 256 ? 256 / T : 1, NW = T / 64;
   constexpr bool GROUPS = KIND == SP24_NORM_FP8_GROUPS;
+  constexpr bool ROWS = KIND == SP24_NORM_FP8_ROWS || KIND == SP24_NORM_INT8_ROWS;
   __shared__ float sh_sum[RPB * NW];
-  __shared__ uint32_t sh_max[RPB * NW];
+  __shared__ uint32_t sh_max[RPB * NW], sh_max2[RPB * NW];
   extern __shared__ uint32_t gmax[];  // [RPB][groups], only where a group is more than a segment
 
   const int tl = threadIdx.x % T, rl = threadIdx.x / T, lane = threadIdx.x & 63;
@@ -87,12 +101,27 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rmsnorm_kernel(
   }
 
   // vectors are loaded B at a time: all of a long row's at once would not fit in the registers
-  // beside u (1024 x 65536 to E4M3: 134 us, in pairs 43)
+  // beside u (1024 x 65536 to E4M3: 134 us, in pairs 43, with the weight loaded again 49)
   constexpr int B = NV > 4 ? 2 : NV;
-  constexpr bool KEEP_W = KIND == SP24_NORM_BF16 && NV <= 4;  // the weight for the output (longer rows load it again)
+  constexpr bool KEEP_W = NV <= 4;  // the weight for the output (longer rows load it again, a vector ahead)
   u32x4 wd[KEEP_W ? NV : B];
-  float u[NV][8], ss = 0.0f;
+  float u[NV][8], ss = 0.0f;  // u: t, until the output
   uint32_t key = 0, gkey[NV];
+  bool off = false;  // groups: a segment's maximum is out of range
+
+  // a group's maximum from its lanes' (in LDS where a group is more than a segment)
+  auto group_max = [&](uint32_t mk) {
+    if (seg > 1) mk = fold_lanes<1>(mk, bits_max);
+    if (seg > 2) mk = fold_lanes<2>(mk, bits_max);
+    if (seg > 4) mk = fold_lanes<4>(mk, bits_max);
+    if (seg > 8) mk = fold_lanes<8>(mk, bits_max);
+    if (seg > 16) mk = fold_lanes<16>(mk, bits_max);
+    if (seg > 32) mk = fold_lanes<32>(mk, bits_max);
+    return mk;
+  };
+  auto collect = [&](uint32_t mk, int i) {
+    if (in_lds && i < nv && lane % seg == 0) atomicMax(&gmax[rl * ng + group_of(i)], mk);
+  };
 #pragma unroll
   for (int j0 = 0; j0 < NV; j0 += B) {
     u32x4 xd[B], rd[B];
@@ -112,10 +141,8 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rmsnorm_kernel(
       uint32_t mk = 0;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const uint32_t xe = (e & 1) ? xd[b][e / 2] & 0xFFFF0000u : xd[b][e / 2] << 16;
-        const uint32_t re = (e & 1) ? rd[b][e / 2] & 0xFFFF0000u : rd[b][e / 2] << 16;
-        float t = __uint_as_float(xe);
-        if (residual != nullptr) t += __uint_as_float(re);
+        float t = bf16_of(xd[b], e);
+        if (residual != nullptr) t += bf16_of(rd[b], e);
         ss = __builtin_fmaf(t, t, ss);
         u[j][e] = t;
       }
@@ -124,23 +151,15 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rmsnorm_kernel(
                       f32x2_to_bf16x2(u[j][4], u[j][5]), f32x2_to_bf16x2(u[j][6], u[j][7])};
         __builtin_nontemporal_store(o, reinterpret_cast<u32x4*>(residual_out) + base + i);
       }
+      if constexpr (ROWS || GROUPS) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t we = (e & 1) ? wd[b][e / 2] & 0xFFFF0000u : wd[b][e / 2] << 16;
-        // bf16 output keeps t (v = t rstd w, as the formula reads); the others u = t w
-        if constexpr (KIND != SP24_NORM_BF16) u[j][e] *= __uint_as_float(we);
-        mk = max(mk, __float_as_uint(u[j][e]) & 0x7FFFFFFFu);
+        for (int e = 0; e < 8; ++e) mk = max(mk, __float_as_uint(u[j][e] * bf16_of(wd[b], e)) & 0x7FFFFFFFu);
+        key = max(key, mk);
       }
-      key = max(key, mk);
       if constexpr (GROUPS) {
-        if (seg > 1) mk = fold_lanes<1>(mk, bits_max);
-        if (seg > 2) mk = fold_lanes<2>(mk, bits_max);
-        if (seg > 4) mk = fold_lanes<4>(mk, bits_max);
-        if (seg > 8) mk = fold_lanes<8>(mk, bits_max);
-        if (seg > 16) mk = fold_lanes<16>(mk, bits_max);
-        if (seg > 32) mk = fold_lanes<32>(mk, bits_max);
-        gkey[j] = mk;
-        if (in_lds && i < nv && lane % seg == 0) atomicMax(&gmax[rl * ng + group_of(i)], mk);
+        gkey[j] = group_max(mk);
+        off = off || (i < nv && out_of_range(gkey[j]));
+        collect(gkey[j], i);
       }
     }
     if constexpr (B < NV) {  // finish this batch: its maximum now, not at the end
@@ -150,7 +169,8 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rmsnorm_kernel(
   }
 
   ss = __uint_as_float(fold_wave(__float_as_uint(ss), bits_sum));
-  if constexpr (!GROUPS) key = fold_wave(key, bits_max);
+  if constexpr (ROWS) key = fold_wave(key, bits_max);
+  if constexpr (GROUPS) key = __any(off) ? 1u : 0u;
   if constexpr (NW > 1) {
     if (lane == 0) {
       sh_sum[threadIdx.x / 64] = ss;
@@ -164,36 +184,104 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rmsnorm_kernel(
       ss += sh_sum[rl * NW + i];
       key = max(key, sh_max[rl * NW + i]);
     }
-  } else {
-    if (in_lds) __syncthreads();
+  } else if (in_lds) {
+    if (lane == 0) sh_max[threadIdx.x / 64] = key;
+    __syncthreads();
   }
   const float rstd = 1.0f / __builtin_sqrtf(ss / (float)k + eps);
 
+  auto weight = [&](int j) {
+    if constexpr (KEEP_W) {
+      return wd[j];
+    } else {
+      const int i = tl + j * T;
+      return i < nv ? reinterpret_cast<const u32x4*>(w)[i] : u32x4{0u, 0u, 0u, 0u};
+    }
+  };
+  bool again = false;  // this row's maxima are those of |t rstd w|
+  if constexpr (ROWS || GROUPS) {
+    auto bad = [&](uint32_t row_key) { return GROUPS ? row_key != 0 : out_of_range(row_key); };
+    again = nv > 0 && bad(key);
+    // barriers are the workgroup's: all its rows come along, those in range keep what they have
+    bool any_again = again;
+    if constexpr (RPB > 1) {
+      if (NW > 1 || in_lds) {
+#pragma unroll
+        for (int r = 0; r < RPB; ++r) {
+          uint32_t rk = 0;
+#pragma unroll
+          for (int i = 0; i < NW; ++i) rk = max(rk, sh_max[r * NW + i]);
+          any_again = any_again || ((int64_t)blockIdx.x * RPB + r < m && bad(rk));
+        }
+      }
+    }
+    auto largest = [&](int j) {
+      const u32x4 wj = weight(j);
+      uint32_t mk = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) mk = max(mk, __float_as_uint(u[j][e] * rstd * bf16_of(wj, e)) & 0x7FFFFFFFu);
+      return mk;
+    };
+    if (any_again) {
+      if constexpr (ROWS) {
+        uint32_t mk = 0;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) mk = max(mk, largest(j));
+        mk = fold_wave(mk, bits_max);
+        if constexpr (NW > 1) {
+          if (lane == 0) sh_max2[threadIdx.x / 64] = mk;
+          __syncthreads();
+          mk = 0;
+#pragma unroll
+          for (int i = 0; i < NW; ++i) mk = max(mk, sh_max2[rl * NW + i]);
+        }
+        if (again) key = mk;
+      } else {
+        if (in_lds) {
+          if (again)
+            for (int i = tl; i < ng; i += T) gmax[rl * ng + i] = 0;
+          __syncthreads();
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          const uint32_t mk = group_max(largest(j));
+          if (again) {
+            gkey[j] = mk;
+            collect(mk, tl + j * T);
+          }
+        }
+        if (in_lds) __syncthreads();
+      }
+    }
+  }
+
+  // v = (t pre) w post: where the maxima are of |t w|, rstd goes to the scale alone
+  const bool in_scale = (ROWS || GROUPS) && !again;
+  const float pre = in_scale ? 1.0f : rstd, post = in_scale ? rstd : 1.0f;
   NormDiv d{0.0f, 0.0f, 1.0f, false};
-  if constexpr (KIND == SP24_NORM_FP8_ROWS || KIND == SP24_NORM_INT8_ROWS) {
-    const float s = norm_scale<KIND>(key, rstd, d);
+  if constexpr (ROWS) {
+    const float s = norm_scale<KIND>(key, post, d);
     if (tl == 0 && nv > 0) static_cast<float*>(scales)[row] = s;
   }
+  u32x4 wnext = weight(0);
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int i = tl + j * T;
+    const u32x4 wj = wnext;
+    if (j + 1 < NV) wnext = weight(j + 1);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) u[j][e] = u[j][e] * pre * bf16_of(wj, e);
     if constexpr (KIND == SP24_NORM_BF16) {
       if (i < nv) {
-        const u32x4 wj = KEEP_W ? wd[KEEP_W ? j : 0] : reinterpret_cast<const u32x4*>(w)[i];
         u32x4 o;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          o[e] = f32x2_to_bf16x2(u[j][2 * e] * rstd * __uint_as_float(wj[e] << 16),
-                                 u[j][2 * e + 1] * rstd * __uint_as_float(wj[e] & 0xFFFF0000u));
+        for (int e = 0; e < 4; ++e) o[e] = f32x2_to_bf16x2(u[j][2 * e], u[j][2 * e + 1]);
         __builtin_nontemporal_store(o, static_cast<u32x4*>(out) + base + i);
       }
     } else if constexpr (KIND == SP24_NORM_MXFP4) {
       uint32_t mk = 0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        u[j][e] *= rstd;
-        mk = max(mk, __float_as_uint(u[j][e]) & 0x7FFFFFFFu);
-      }
+      for (int e = 0; e < 8; ++e) mk = max(mk, __float_as_uint(u[j][e]) & 0x7FFFFFFFu);
       const uint32_t byte = mx4_block_byte<23>(mk);  // k % 128 == 0: the 16 lanes of a word are all in the row
       const uint32_t word = mx4_word_of_blocks(byte, lane);
       if (i < nv) {
@@ -204,7 +292,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rmsnorm_kernel(
       if (i < nv) {
         if constexpr (GROUPS) {
           const int g = group_of(i);
-          const float s = norm_scale<KIND>(in_lds ? gmax[rl * ng + g] : gkey[j], rstd, d);
+          const float s = norm_scale<KIND>(in_lds ? gmax[rl * ng + g] : gkey[j], post, d);
           if (i == g * vpg) static_cast<float*>(scales)[(size_t)row * ng + g] = s;
         }
         __builtin_nontemporal_store(norm_codes8<KIND>(u[j], d), static_cast<u32x2*>(out) + base + i);
