@@ -7,6 +7,8 @@
 // what a tensor is, and the package's error class (set_error) for a status of the library.
 #define PY_SSIZE_T_CLEAN
 #include <ATen/ops/empty.h>
+#include <c10/hip/HIPException.h>
+#include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -312,12 +314,37 @@ void place(const Function& f, PyObject* const* args, Py_ssize_t count, PyObject*
     }
 }
 
-// No C++ exception leaves a function: what torch throws becomes a RuntimeError.
+// A GPU made the current one for a scope (-1: none); where it is that already, one query.
+class Current {
+ public:
+  explicit Current(c10::DeviceIndex device) {
+    c10::DeviceIndex now = 0;
+    if (device < 0) return;
+    C10_HIP_CHECK(c10::hip::GetDevice(&now));
+    if (now == device) return;
+    C10_HIP_CHECK(c10::hip::SetDevice(device));
+    was_ = now;
+  }
+  ~Current() {
+    if (was_ >= 0) C10_HIP_CHECK_WARN(c10::hip::SetDevice(was_));
+  }
+  Current(const Current&) = delete;
+  Current& operator=(const Current&) = delete;
+
+ private:
+  c10::DeviceIndex was_ = -1;
+};
+
+// No C++ exception leaves a function: what torch throws becomes a RuntimeError.  The first
+// argument's GPU is the current one for the call (the default stream's handle is the same on
+// all of them: a launch goes to the current one), and its other tensors have to be there too.
 template <Function& F>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t count, PyObject* names) {
   try {
     PyObject* a[kMost];
     place(F, args, count, names, a);
+    const bool gpu = THPVariable_Check(a[0]) && THPVariable_Unpack(a[0]).is_cuda();
+    const Current on(gpu ? THPVariable_Unpack(a[0]).device().index() : (c10::DeviceIndex)-1);
     return F.call(a);
   } catch (const Failed&) {
   } catch (const std::exception& e) {
