@@ -155,10 +155,20 @@ def _ptr(t):
 
 # the current stream's handle without building a Stream object (2 us a call)
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
-def _stream(dev):
-    return _raw_stream(dev.index)
+def _launch(fn, dev, *args):
+    """Calls `fn` of the library on the current stream of `dev`, with `dev` the current GPU: the default
+    stream's handle is the same on every GPU, and a launch on it goes to the current one."""
+    f, index = getattr(lib, fn), dev.index
+    if _current_device() == index:
+        status = f(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            status = f(*args, _raw_stream(index))
+    if status != 0:
+        raise Sp24Error(fn, status)
 
 
 def _need(t, name, dtype=None, ndim=None, device=None):
@@ -237,8 +247,7 @@ def prune_compress(w: torch.Tensor, values: torch.Tensor | None = None,
     _need(values, "values", torch.bfloat16, 2, w.device)
     _need(meta, "meta", torch.int32, 1, w.device)
     _meta_size(meta, n, k)
-    _check("sp24_prune_compress",
-           lib.sp24_prune_compress(_ptr(w), n, k, _ptr(values), _ptr(meta), _stream(w.device)))
+    _launch("sp24_prune_compress", w.device, _ptr(w), n, k, _ptr(values), _ptr(meta))
     return values, meta
 
 
@@ -254,8 +263,7 @@ def decompress(values: torch.Tensor, meta: torch.Tensor, k: int, out: torch.Tens
         t = torch.bfloat16 if dt == BF16 else torch.int8 if dt == INT8 else torch.uint8
         out = torch.empty(n, k, dtype=t, device=values.device)
     _need(out, "out", _tensor_types(dt), 2, values.device)
-    _check("sp24_decompress",
-           lib.sp24_decompress(dt, _ptr(values), _ptr(meta), n, k, _ptr(out), _stream(values.device)))
+    _launch("sp24_decompress", values.device, dt, _ptr(values), _ptr(meta), n, k, _ptr(out))
     return out
 
 
@@ -269,8 +277,7 @@ def check_meta(meta: torch.Tensor, k: int, bad: torch.Tensor | None = None) -> t
     if bad is None:
         bad = torch.zeros(1, dtype=torch.int32, device=meta.device)
     _need(bad, "bad", torch.int32, None, meta.device)
-    _check("sp24_check_meta",
-           lib.sp24_check_meta(_ptr(meta), meta.numel() // words, k, _ptr(bad), _stream(meta.device)))
+    _launch("sp24_check_meta", meta.device, _ptr(meta), meta.numel() // words, k, _ptr(bad))
     return bad
 
 
@@ -299,9 +306,7 @@ def quant_fp8(x: torch.Tensor, scale: torch.Tensor | None = None, out: torch.Ten
     _need_scalar(scale, "scale")
     nbytes = workspace_size(OP_QUANT, BF16, count, 1, 1) if mode == SCALE_DYNAMIC else 0
     ws = _workspace(nbytes, x.device, ws)
-    _check("sp24_quant_fp8",
-           lib.sp24_quant_fp8(_ptr(x), count, _ptr(out), _ptr(scale), mode, _ptr(ws), nbytes,
-                              _stream(x.device)))
+    _launch("sp24_quant_fp8", x.device, _ptr(x), count, _ptr(out), _ptr(scale), mode, _ptr(ws), nbytes)
     return out, scale
 
 
@@ -326,9 +331,7 @@ def quant_int8(x: torch.Tensor, scale: torch.Tensor | None = None, out: torch.Te
     _need_scalar(scale, "scale")
     nbytes = workspace_size(OP_QUANT, BF16, count, 1, 1) if mode == SCALE_DYNAMIC else 0
     ws = _workspace(nbytes, x.device, ws)
-    _check("sp24_quant_int8",
-           lib.sp24_quant_int8(_ptr(x), count, _ptr(out), _ptr(scale), mode, _ptr(ws), nbytes,
-                               _stream(x.device)))
+    _launch("sp24_quant_int8", x.device, _ptr(x), count, _ptr(out), _ptr(scale), mode, _ptr(ws), nbytes)
     return out, scale
 
 
@@ -363,13 +366,9 @@ def _gemm(sparse, x, w, meta, x_scale, w_scale, out, ws):
     xs = _ptr(x_scale) if dt != BF16 else None
     wsc = _ptr(w_scale) if dt != BF16 else None
     if sparse:
-        st = lib.sp24_gemm(dt, m, n, k, _ptr(x), xs, _ptr(w), _ptr(meta), wsc, _ptr(out), _ptr(ws),
-                           nbytes, _stream(x.device))
-        _check("sp24_gemm", st)
+        _launch("sp24_gemm", x.device, dt, m, n, k, _ptr(x), xs, _ptr(w), _ptr(meta), wsc, _ptr(out), _ptr(ws), nbytes)
     else:
-        st = lib.sp24_dense_gemm(dt, m, n, k, _ptr(x), xs, _ptr(w), wsc, _ptr(out), _ptr(ws), nbytes,
-                                 _stream(x.device))
-        _check("sp24_dense_gemm", st)
+        _launch("sp24_dense_gemm", x.device, dt, m, n, k, _ptr(x), xs, _ptr(w), wsc, _ptr(out), _ptr(ws), nbytes)
     return out
 
 
@@ -393,8 +392,7 @@ def quant_fp8_rows(x: torch.Tensor, out: torch.Tensor | None = None, scales: tor
     _need(scales, "scales", torch.float32, 1, x.device)
     if scales.numel() != m:
         raise ValueError("scales must hold %d values" % m)
-    _check("sp24_quant_fp8_rows", lib.sp24_quant_fp8_rows(_ptr(x), m, k, _ptr(out), _ptr(scales),
-                                                          _stream(x.device)))
+    _launch("sp24_quant_fp8_rows", x.device, _ptr(x), m, k, _ptr(out), _ptr(scales))
     return out, scales
 
 
@@ -413,8 +411,7 @@ def quant_int8_rows(x: torch.Tensor, out: torch.Tensor | None = None, scales: to
     _need(scales, "scales", torch.float32, 1, x.device)
     if scales.numel() != m:
         raise ValueError("scales must hold %d values" % m)
-    _check("sp24_quant_int8_rows", lib.sp24_quant_int8_rows(_ptr(x), m, k, _ptr(out), _ptr(scales),
-                                                            _stream(x.device)))
+    _launch("sp24_quant_int8_rows", x.device, _ptr(x), m, k, _ptr(out), _ptr(scales))
     return out, scales
 
 
@@ -427,8 +424,7 @@ def slide_prune_pack(w: torch.Tensor, n_pat: int = 4, out: torch.Tensor | None =
     if out is None:
         out = torch.empty(n, max(kp, 1), dtype=torch.bfloat16, device=w.device)
     _need(out, "out", torch.bfloat16, 2, w.device)
-    _check("sp24_slide_prune_pack", lib.sp24_slide_prune_pack(_ptr(w), n, k, n_pat, _ptr(out),
-                                                              _stream(w.device)))
+    _launch("sp24_slide_prune_pack", w.device, _ptr(w), n, k, n_pat, _ptr(out))
     return out
 
 
@@ -445,8 +441,7 @@ def slide_quant_fp8_rows(x: torch.Tensor, n_pat: int = 4, out: torch.Tensor | No
     if scales is None:
         scales = torch.empty(m, dtype=torch.float32, device=x.device)
     _need(scales, "scales", torch.float32, 1, x.device)
-    _check("sp24_slide_quant_fp8_rows", lib.sp24_slide_quant_fp8_rows(_ptr(x), m, k, n_pat, _ptr(out),
-                                                                      _ptr(scales), _stream(x.device)))
+    _launch("sp24_slide_quant_fp8_rows", x.device, _ptr(x), m, k, n_pat, _ptr(out), _ptr(scales))
     return out, scales
 
 
@@ -463,8 +458,7 @@ def slide_quant_int8_rows(x: torch.Tensor, n_pat: int = 4, out: torch.Tensor | N
     if scales is None:
         scales = torch.empty(m, dtype=torch.float32, device=x.device)
     _need(scales, "scales", torch.float32, 1, x.device)
-    _check("sp24_slide_quant_int8_rows", lib.sp24_slide_quant_int8_rows(_ptr(x), m, k, n_pat, _ptr(out),
-                                                                        _ptr(scales), _stream(x.device)))
+    _launch("sp24_slide_quant_int8_rows", x.device, _ptr(x), m, k, n_pat, _ptr(out), _ptr(scales))
     return out, scales
 
 
@@ -493,8 +487,8 @@ def gemm_rows(x, values, meta, x_scales, w_scale, out=None, ws=None):
         raise ValueError("out must be [%d, %d]" % (m, n))
     nbytes = workspace_size(OP_GEMM, dt, m, n, k)
     ws = _workspace(nbytes, x.device, ws)
-    _check("sp24_gemm_rows", lib.sp24_gemm_rows(dt, m, n, k, _ptr(x), _ptr(x_scales), _ptr(values), _ptr(meta),
-                                                _ptr(w_scale), _ptr(out), _ptr(ws), nbytes, _stream(x.device)))
+    _launch("sp24_gemm_rows", x.device, dt, m, n, k, _ptr(x), _ptr(x_scales), _ptr(values), _ptr(meta), _ptr(w_scale),
+            _ptr(out), _ptr(ws), nbytes)
     return out
 
 
@@ -523,8 +517,8 @@ def gemm_qx(x, values, meta, w_scale, x_scale=None, out=None, ws=None):
         raise ValueError("out must be [%d, %d]" % (m, n))
     nbytes = workspace_size(OP_GEMM_QX, FP8, m, n, k)
     ws = _workspace(nbytes, x.device, ws)
-    _check("sp24_gemm_qx", lib.sp24_gemm_qx(m, n, k, _ptr(x), _ptr(x_scale), _ptr(values), _ptr(meta),
-                                            _ptr(w_scale), _ptr(out), _ptr(ws), nbytes, _stream(x.device)))
+    _launch("sp24_gemm_qx", x.device, m, n, k, _ptr(x), _ptr(x_scale), _ptr(values), _ptr(meta), _ptr(w_scale),
+            _ptr(out), _ptr(ws), nbytes)
     return out, x_scale
 
 
@@ -548,9 +542,8 @@ def gemm_qx_noalloc(x, values, meta, w_scale, x_scale, out):
     _need(out, "out", torch.bfloat16, 2, x.device)
     if out.shape != (m, n):
         raise ValueError("out must be [%d, %d]" % (m, n))
-    _check("sp24_gemm_qx_noalloc", lib.sp24_gemm_qx_noalloc(m, n, k, _ptr(x), _ptr(x_scale), _ptr(values),
-                                                            _ptr(meta), _ptr(w_scale), _ptr(out),
-                                                            _stream(x.device)))
+    _launch("sp24_gemm_qx_noalloc", x.device, m, n, k, _ptr(x), _ptr(x_scale), _ptr(values), _ptr(meta),
+            _ptr(w_scale), _ptr(out))
     return out, x_scale
 
 
@@ -576,8 +569,7 @@ def quant_fp8_groups(x: torch.Tensor, group: int, out: torch.Tensor | None = Non
     _need(scales, "scales", torch.float32, None, x.device)
     if scales.numel() != rows * (cols // group):
         raise ValueError("scales must hold %d values" % (rows * (cols // group)))
-    _check("sp24_quant_fp8_groups", lib.sp24_quant_fp8_groups(_ptr(x), rows, cols, group, _ptr(out), _ptr(scales),
-                                                              _stream(x.device)))
+    _launch("sp24_quant_fp8_groups", x.device, _ptr(x), rows, cols, group, _ptr(out), _ptr(scales))
     return out, scales
 
 
@@ -608,8 +600,8 @@ def gemm_groups(x, x_scales, values, meta, w_scales, group, out=None, ws=None):
         raise ValueError("out must be [%d, %d]" % (m, n))
     nbytes = workspace_size(OP_GEMM_GROUPS, FP8, m, n, k)
     ws = _workspace(nbytes, x.device, ws)
-    _check("sp24_gemm_groups", lib.sp24_gemm_groups(m, n, k, group, _ptr(x), _ptr(x_scales), _ptr(values), _ptr(meta),
-                                                    _ptr(w_scales), _ptr(out), _ptr(ws), nbytes, _stream(x.device)))
+    _launch("sp24_gemm_groups", x.device, m, n, k, group, _ptr(x), _ptr(x_scales), _ptr(values), _ptr(meta),
+            _ptr(w_scales), _ptr(out), _ptr(ws), nbytes)
     return out
 
 
@@ -645,9 +637,8 @@ def gemm_rows_qx(x, values, meta, w_scale, x_scales=None, out=None, ws=None):
     m, n, x_scales, out = _rows_qx_args(x, values, meta, w_scale, k, x_scales, out)
     nbytes = workspace_size(OP_GEMM_ROWS_QX, FP8, m, n, k)
     ws = _workspace(nbytes, x.device, ws)
-    _check("sp24_gemm_rows_qx", lib.sp24_gemm_rows_qx(m, n, k, _ptr(x), _ptr(x_scales), _ptr(values), _ptr(meta),
-                                                      _ptr(w_scale), _ptr(out), _ptr(ws), nbytes,
-                                                      _stream(x.device)))
+    _launch("sp24_gemm_rows_qx", x.device, m, n, k, _ptr(x), _ptr(x_scales), _ptr(values), _ptr(meta), _ptr(w_scale),
+            _ptr(out), _ptr(ws), nbytes)
     return out, x_scales
 
 
@@ -661,9 +652,8 @@ def slide_gemm_qx(x, values, meta, w_scale, n_pat=4, x_scales=None, out=None, ws
     m, n, x_scales, out = _rows_qx_args(x, values, meta, w_scale, kp, x_scales, out)
     nbytes = workspace_size(OP_GEMM_ROWS_QX, FP8, m, n, kp)
     ws = _workspace(nbytes, x.device, ws)
-    _check("sp24_slide_gemm_qx", lib.sp24_slide_gemm_qx(n_pat, m, n, k, _ptr(x), _ptr(x_scales), _ptr(values),
-                                                        _ptr(meta), _ptr(w_scale), _ptr(out), _ptr(ws), nbytes,
-                                                        _stream(x.device)))
+    _launch("sp24_slide_gemm_qx", x.device, n_pat, m, n, k, _ptr(x), _ptr(x_scales), _ptr(values), _ptr(meta),
+            _ptr(w_scale), _ptr(out), _ptr(ws), nbytes)
     return out, x_scales
 
 
@@ -711,8 +701,7 @@ def palette_encode(w: torch.Tensor, ws: torch.Tensor | None = None) -> PaletteWe
     if nbytes == 0:
         raise ValueError("palette weights need n >= 1 and k % 128 == 0 (got %d x %d)" % (n, k))
     ws = _workspace(nbytes, dev, ws)
-    _check("sp24_palette_analyze", lib.sp24_palette_analyze(_ptr(w), n, k, _ptr(pal), _ptr(slot), _ptr(counts),
-                                                            _ptr(ws), nbytes, _stream(dev)))
+    _launch("sp24_palette_analyze", dev, _ptr(w), n, k, _ptr(pal), _ptr(slot), _ptr(counts), _ptr(ws), nbytes)
     n_pal, n_verb = (int(v) for v in counts.cpu().tolist())
     pad = lambda r: (r + 15) // 16 * 16
     sm = torch.zeros(pad(n_pal) * k, dtype=torch.uint8, device=dev)
@@ -721,8 +710,8 @@ def palette_encode(w: torch.Tensor, ws: torch.Tensor | None = None) -> PaletteWe
     verb = torch.zeros(pad(n_verb) * k, dtype=torch.bfloat16, device=dev)
     verb_rows = torch.empty(n_verb, dtype=torch.int32, device=dev)
     p = lambda t: _ptr(t) if t.numel() else None
-    _check("sp24_palette_pack", lib.sp24_palette_pack(_ptr(w), n, k, _ptr(pal), _ptr(slot), n_pal, n_verb, p(sm),
-                                                      p(ix), p(pal_rows), p(verb), p(verb_rows), _stream(dev)))
+    _launch("sp24_palette_pack", dev, _ptr(w), n, k, _ptr(pal), _ptr(slot), n_pal, n_verb, p(sm), p(ix), p(pal_rows),
+            p(verb), p(verb_rows))
     return PaletteWeight(n, k, pal, pal_rows, sm, ix, verb_rows, verb)
 
 
@@ -733,7 +722,7 @@ def palette_decode(pw: PaletteWeight, out: torch.Tensor | None = None) -> torch.
         out = torch.empty(pw.n, pw.k, dtype=torch.bfloat16, device=dev)
     _need(out, "out", torch.bfloat16, 2, dev)
     st = pw.struct()
-    _check("sp24_palette_decode", lib.sp24_palette_decode(ctypes.byref(st), pw.n, pw.k, _ptr(out), _stream(dev)))
+    _launch("sp24_palette_decode", dev, ctypes.byref(st), pw.n, pw.k, _ptr(out))
     return out
 
 
@@ -753,8 +742,7 @@ def palette_gemm(x: torch.Tensor, pw: PaletteWeight, out: torch.Tensor | None = 
     nbytes = workspace_size(OP_PALETTE_GEMM, BF16, m, pw.n, k)
     ws = _workspace(nbytes, x.device, ws)
     st = pw.struct()
-    _check("sp24_palette_gemm", lib.sp24_palette_gemm(m, pw.n, k, _ptr(x), ctypes.byref(st), _ptr(out), _ptr(ws),
-                                                      nbytes, _stream(x.device)))
+    _launch("sp24_palette_gemm", x.device, m, pw.n, k, _ptr(x), ctypes.byref(st), _ptr(out), _ptr(ws), nbytes)
     return out
 
 
@@ -800,17 +788,14 @@ def probe_mfma_layout(variant: int, a: torch.Tensor, b: torch.Tensor, idx: torch
         raise ValueError("a/b too small")
     if idx.numel() * idx.element_size() < n_exp * 64 * 4 or c.numel() * c.element_size() < n_exp * 64 * 64:
         raise ValueError("idx/c too small")
-    _check("sp24_probe_mfma_layout",
-           lib.sp24_probe_mfma_layout(variant, _ptr(a), _ptr(b), _ptr(idx), _ptr(c), n_exp,
-                                      _stream(a.device)))
+    _launch("sp24_probe_mfma_layout", a.device, variant, _ptr(a), _ptr(b), _ptr(idx), _ptr(c), n_exp)
 
 
 def probe_mfma_rate(variant: int, iters: int, blocks: int, waves: int, out: torch.Tensor):
     _need(out, "out", torch.float32)
     if out.numel() < blocks * waves * 64:
         raise ValueError("out too small")
-    _check("sp24_probe_mfma_rate",
-           lib.sp24_probe_mfma_rate(variant, iters, blocks, waves, _ptr(out), _stream(out.device)))
+    _launch("sp24_probe_mfma_rate", out.device, variant, iters, blocks, waves, _ptr(out))
 
 
 def probe_copy(src: torch.Tensor, dst: torch.Tensor):
@@ -819,7 +804,7 @@ def probe_copy(src: torch.Tensor, dst: torch.Tensor):
     nbytes = src.numel() * src.element_size()
     if dst.numel() * dst.element_size() < nbytes:
         raise ValueError("dst too small")
-    _check("sp24_probe_copy", lib.sp24_probe_copy(_ptr(src), _ptr(dst), nbytes, _stream(src.device)))
+    _launch("sp24_probe_copy", src.device, _ptr(src), _ptr(dst), nbytes)
 
 
 def probe_ring(w_kb: int, x_kb: int, stages: int, barrier: bool, w: torch.Tensor, w_stride: int,
@@ -834,9 +819,8 @@ def probe_ring(w_kb: int, x_kb: int, stages: int, barrier: bool, w: torch.Tensor
         raise ValueError("out too small")
     if w_kb > 0 and w.numel() * w.element_size() < (blocks - 1) * w_stride + steps * w_kb * 1024:
         raise ValueError("w too small")
-    _check("sp24_probe_ring",
-           lib.sp24_probe_ring(w_kb, x_kb, stages, 1 if barrier else 0, _ptr(w), w_stride, _ptr(x),
-                               x.numel() * x.element_size(), blocks, steps, _ptr(out), _stream(w.device)))
+    _launch("sp24_probe_ring", w.device, w_kb, x_kb, stages, 1 if barrier else 0, _ptr(w), w_stride, _ptr(x),
+            x.numel() * x.element_size(), blocks, steps, _ptr(out))
 
 
 def probe_read(src: torch.Tensor, out: torch.Tensor):
@@ -844,5 +828,4 @@ def probe_read(src: torch.Tensor, out: torch.Tensor):
     _need(out, "out", torch.int32, None, src.device)
     if out.numel() < lib.sp24_probe_read_blocks():
         raise ValueError("out too small")
-    _check("sp24_probe_read",
-           lib.sp24_probe_read(_ptr(src), src.numel() * src.element_size(), _ptr(out), _stream(src.device)))
+    _launch("sp24_probe_read", src.device, _ptr(src), src.numel() * src.element_size(), _ptr(out))

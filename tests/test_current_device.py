@@ -26,7 +26,7 @@ def runtime(tmp_path_factory):
     return out
 
 
-@pytest.mark.parametrize("group", ["mxfp4"])
+@pytest.mark.parametrize("group", ["mxfp4", "sparse"])
 def test_launches_go_to_the_tensors_device(runtime, group):
     r = subprocess.run([sys.executable, os.path.join(HERE, "two_gpus.py"), runtime, group], capture_output=True,
                        text=True, timeout=300)

@@ -46,6 +46,45 @@ def mxfp4():
     }
 
 
+def sparse():
+    x, w, u8, f32, i32 = new((M, K)), new((N, K)), torch.uint8, torch.float32, torch.int32
+    v, meta, one = new((N, K // 2)), new(N * K // 32, i32), new(1, f32)
+    q, qv, qw = new((M, K), u8), new((N, K // 2), u8), new((N, K), u8)
+    xs, kp = new(M, f32), K // 8 * 12  # k of a 6:8 weight lifted to 2:4 windows
+    sv, sm = new((N, kp // 2), u8), new(N * kp // 32, i32)
+    pw = sp.PaletteWeight(N, K, new(16, u8), torch.empty(N, dtype=i32, device="cuda:1"), new(N * K, u8),
+                          new(N * K // 8, i32), new(0, i32), new(0))
+    big = new(1 << 20, u8)
+    return {
+        "prune_compress": lambda: sp.prune_compress(w),
+        "decompress": lambda: sp.decompress(v, meta, K),
+        "check_meta": lambda: sp.check_meta(meta, K, new(1, i32)),
+        "quant_fp8": lambda: sp.quant_fp8(x),
+        "quant_int8": lambda: sp.quant_int8(x),
+        "gemm": lambda: sp.gemm(x, v, meta),
+        "dense_gemm": lambda: sp.dense_gemm(x, w),
+        "quant_fp8_rows": lambda: sp.quant_fp8_rows(x),
+        "quant_int8_rows": lambda: sp.quant_int8_rows(x),
+        "slide_prune_pack": lambda: sp.slide_prune_pack(w),
+        "slide_quant_fp8_rows": lambda: sp.slide_quant_fp8_rows(x),
+        "slide_quant_int8_rows": lambda: sp.slide_quant_int8_rows(x),
+        "gemm_rows": lambda: sp.gemm_rows(q, qv, meta, xs, one),
+        "gemm_qx": lambda: sp.gemm_qx(x, qv, meta, one),
+        "gemm_qx_noalloc": lambda: sp.gemm_qx_noalloc(x, qv, meta, one, new(1, f32), new((M, N))),
+        "quant_fp8_groups": lambda: sp.quant_fp8_groups(x, 128),
+        "gemm_groups": lambda: sp.gemm_groups(q, new((M, K // 128), f32), qv, meta, new((N, K // 128), f32), 128),
+        "gemm_rows_qx": lambda: sp.gemm_rows_qx(x, qv, meta, one),
+        "slide_gemm_qx": lambda: sp.slide_gemm_qx(x, sv, sm, one),
+        "palette_decode": lambda: sp.palette_decode(pw),
+        "palette_gemm": lambda: sp.palette_gemm(x, pw),
+        "probe_mfma_layout": lambda: sp.probe_mfma_layout(0, big, big, big, big, 1),
+        "probe_mfma_rate": lambda: sp.probe_mfma_rate(0, 1, 1, 1, new(64, f32)),
+        "probe_copy": lambda: sp.probe_copy(big, new(1 << 20, u8)),
+        "probe_read": lambda: sp.probe_read(big, new(1 << 20, i32)),
+        "probe_ring": lambda: sp.probe_ring(8, 16, 4, True, big, 8 << 10, big, 1, 1, new(1, i32)),
+    }
+
+
 def main():
     torch.cuda.set_device(0)
     got = {}
