@@ -6,7 +6,8 @@ the C++ module _sp24): every call checks dtypes, devices, shapes and contiguity
 of torch tensors, passes their device pointers and the current HIP stream, and
 raises on a non-OK status.
 PyTorch is used only for device memory and streams; all arithmetic runs in the
-library's HIP kernels.  If libsp24.so is missing this module raises on import:
+library's HIP kernels.  If libsp24.so is missing this module raises on import, and
+without an _sp24 built for this PyTorch its functions raise when they are called:
 there is no fallback.
 
     values, meta = prune_compress(w)                    # w: [n, k] bf16 on the GPU
@@ -20,6 +21,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import re
 
 import torch
 
@@ -127,8 +129,22 @@ lib.sp24_status_string.restype = ctypes.c_char_p
 
 try:  # the binding of the MXFP4 operators and the norm, in C++ (csrc/sp24_python.cpp)
     from . import _sp24 as _native
-except ImportError as _e:
-    raise ImportError("%s: it is built with libsp24.so by `python bf16_gemm_linear_amd/build.py`" % _e) from _e
+    _built = getattr(_native, "torch_version", "another")
+    if _built != re.match(r"\d+(\.\d+)*", str(torch.__version__)).group():
+        raise ImportError("built for PyTorch %s, not %s" % (_built, torch.__version__))
+except ImportError as _e:  # bound to one PyTorch's C++ interface; what goes through ctypes is not
+    _native, _missing = None, str(_e)
+
+
+def _from_native(name):
+    """The C++ module's function, or where there is none one that says so."""
+    if _native is not None:
+        return getattr(_native, name)
+
+    def absent(*args, **kwargs):
+        raise ImportError("%s needs _sp24.so, which is built with libsp24.so by `python bf16_gemm_linear_amd/build.py` "
+                          "(%s)" % (name, _missing))
+    return absent
 
 
 class Sp24Error(RuntimeError):
@@ -137,7 +153,8 @@ class Sp24Error(RuntimeError):
         super().__init__("%s failed: %s (%d)" % (fn, lib.sp24_status_string(status).decode(), status))
 
 
-_native.set_error(Sp24Error)
+if _native is not None:
+    _native.set_error(Sp24Error)
 
 
 def _check(fn, status):
@@ -154,8 +171,8 @@ def _ptr(t):
 
 
 # the current stream's handle without building a Stream object (2 us a call)
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # (absent from a PyTorch without GPU support)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _launch(fn, dev, *args):
@@ -772,12 +789,12 @@ def mxfp4_scale_index(rows: int, cols: int, device=None) -> torch.Tensor:
 
 
 # the MXFP4 operators and the norm, as the C++ module has them (help() shows their arguments)
-quant_mxfp4 = _native.quant_mxfp4
-dequant_mxfp4 = _native.dequant_mxfp4
-gemm_mxfp4 = _native.gemm_mxfp4
-gated_mxfp4 = _native.gated_mxfp4
-rmsnorm = _native.rmsnorm
-ffn_mxfp4 = _native.ffn_mxfp4
+quant_mxfp4 = _from_native("quant_mxfp4")
+dequant_mxfp4 = _from_native("dequant_mxfp4")
+gemm_mxfp4 = _from_native("gemm_mxfp4")
+gated_mxfp4 = _from_native("gated_mxfp4")
+rmsnorm = _from_native("rmsnorm")
+ffn_mxfp4 = _from_native("ffn_mxfp4")
 
 
 def probe_mfma_layout(variant: int, a: torch.Tensor, b: torch.Tensor, idx: torch.Tensor,

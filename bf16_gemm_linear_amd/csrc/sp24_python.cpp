@@ -11,6 +11,7 @@
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/version.h>
 
 #include "sp24.h"
 
@@ -427,4 +428,12 @@ bool prepare() {
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__sp24() { return prepare() ? PyModule_Create(&g_module) : nullptr; }
+PyMODINIT_FUNC PyInit__sp24() {
+  PyObject* const m = prepare() ? PyModule_Create(&g_module) : nullptr;
+  // for the package to compare: another PyTorch's tensors may be laid out otherwise
+  if (m != nullptr && PyModule_AddStringConstant(m, "torch_version", TORCH_VERSION) != 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}
