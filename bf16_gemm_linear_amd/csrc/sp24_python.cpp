@@ -10,6 +10,7 @@
 #include <c10/hip/HIPException.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/version.h>
 
@@ -336,9 +337,10 @@ class Current {
   c10::DeviceIndex was_ = -1;
 };
 
-// No C++ exception leaves a function: what torch throws becomes a RuntimeError.  The first
-// argument's GPU is the current one for the call (the default stream's handle is the same on
-// all of them: a launch goes to the current one), and its other tensors have to be there too.
+// No C++ exception leaves a function: what torch throws becomes the Python error that torch's
+// own functions raise for it (no memory left: torch.OutOfMemoryError).  The first argument's GPU
+// is the current one for the call (the default stream's handle is the same on all of them, and a
+// launch on it goes to the current one); its other tensors have to be there too.
 template <Function& F>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t count, PyObject* names) {
   try {
@@ -348,8 +350,8 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t count, PyObject* na
     const Current on(gpu ? THPVariable_Unpack(a[0]).device().index() : (c10::DeviceIndex)-1);
     return F.call(a);
   } catch (const Failed&) {
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (const std::exception&) {
+    torch::translate_exception_to_python(std::current_exception());
   } catch (...) {
     PyErr_SetString(PyExc_RuntimeError, "unknown C++ exception");
   }

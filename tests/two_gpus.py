@@ -85,8 +85,25 @@ def sparse():
     }
 
 
+def out_of_memory():
+    """Outputs that no memory is left for: the exceptions of the C++ functions and of a ctypes one."""
+    q = new((1 << 19, 64), torch.uint8), new(1 << 21, torch.uint8)
+    x, v, meta = new((1 << 18, 64)), new((1 << 18, 32)), new(1 << 19, torch.int32)
+    got = {}
+    for name, call in {"gemm_mxfp4": lambda: sp.gemm_mxfp4(*q, *q),
+                       "gated_mxfp4": lambda: sp.gated_mxfp4(*q, *q),
+                       "gemm": lambda: sp.gemm(x, v, meta)}.items():
+        try:
+            call()
+        except Exception as e:
+            got[name] = [t.__name__ for t in type(e).__mro__]
+    print(json.dumps(got))
+
+
 def main():
     torch.cuda.set_device(0)
+    if sys.argv[2] == "out_of_memory":
+        return out_of_memory()
     got = {}
     for name, call in globals()[sys.argv[2]]().items():
         runtime.fake_clear()
