@@ -73,6 +73,19 @@ constexpr Mx4Config kConfigs[] = {
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t ceil_shift(int64_t a, int log) { return (a + ((int64_t)1 << log) - 1) >> log; }
 
+int64_t tiles_of(const Mx4Config& c, const Mx4Args& a) {
+  return ceil_shift(a.n, a.gated ? c.log_n - 1 : c.log_n) * ceil_shift(a.m, c.log_m);
+}
+
+// Whether a configuration can run the call: its tokens, its outputs, and a grid of fewer than 2^32
+// threads, which HIP refuses to launch more of (a gated product of 2^21 x 2^17 outputs, 146 GB in
+// MXFP4, is past it on 128 x 128 tiles and not on 256 x 256).
+bool can_run(const Mx4Config& c, const Mx4Args& a) {
+  const int threads = c.kernel == TILED ? (c.id == 1 ? 512 : 256) : 64 << c.log_kw;
+  return a.m >= c.min_m && a.m <= c.max_m && (!a.gated || (a.hq != nullptr ? c.gated_mx4 : c.gated)) &&
+         tiles_of(c, a) * threads < (int64_t)1 << 32;
+}
+
 // SP24_MX4="stream,row blocks", "wave,configuration" or "tiled,configuration" takes that
 // configuration where it can run the call (tuning and tests only).
 const Mx4Config* forced(const Mx4Args& a, const char* v) {
@@ -82,23 +95,21 @@ const Mx4Config* forced(const Mx4Args& a, const char* v) {
   const Kernel k = strcmp(name, "stream") == 0 ? STREAM : strcmp(name, "wave") == 0 ? WAVE : TILED;
   if (k == TILED && strcmp(name, "tiled") != 0) return nullptr;
   for (const Mx4Config& c : kConfigs)
-    if (c.kernel == k && c.id == id && a.m >= c.min_m && a.m <= c.max_m &&
-        (!a.gated || (a.hq != nullptr ? c.gated_mx4 : c.gated)))
-      return &c;
+    if (c.kernel == k && c.id == id && can_run(c, a)) return &c;
   return nullptr;
 }
 
-const Mx4Config& plan(const Mx4Args& a) {
+const Mx4Config* plan(const Mx4Args& a) {
   const char* v = getenv("SP24_MX4");
   if (v != nullptr && v[0] != '\0')
-    if (const Mx4Config* c = forced(a, v)) return *c;
+    if (const Mx4Config* c = forced(a, v)) return c;
   const Mx4Config* best = nullptr;
   double least = 0;
   const int64_t steps = ceil_shift(a.k, kLogStep);
   const double weight = (a.gated ? 2e-6 : 1e-6) * 0.53 * (double)a.n * a.k, written = 2e-6 * (double)a.m * a.n;
   for (const Mx4Config& c : kConfigs) {
-    if (a.m < c.min_m || a.m > c.max_m || (a.gated && !(a.hq != nullptr ? c.gated_mx4 : c.gated))) continue;
-    const int64_t tiles = ceil_shift(a.n, a.gated ? c.log_n - 1 : c.log_n) * ceil_shift(a.m, c.log_m);
+    if (!can_run(c, a)) continue;
+    const int64_t tiles = tiles_of(c, a);
     const int64_t parts = ceil_shift(tiles << c.log_share, kLogCus);  // rounds, in 1 / share
     const double rounds = parts <= 1 << c.log_share ? 1.0 : (double)parts / (1 << c.log_share);
     const double s = (double)ceil_shift(steps, c.log_kw);
@@ -109,13 +120,15 @@ const Mx4Config& plan(const Mx4Args& a) {
       least = t;
     }
   }
-  return *best;
+  return best;
 }
 
 }  // namespace
 
 hipError_t launch_mx4_gemm(const Mx4Args& a, hipStream_t s) {
-  const Mx4Config& c = plan(a);
+  const Mx4Config* const best = plan(a);
+  if (best == nullptr) return hipErrorInvalidConfiguration;  // more outputs than the card's memory holds
+  const Mx4Config& c = *best;
   if (c.kernel == WAVE) return launch_mx4_wave(c.id, a, s);
   if (c.kernel == TILED) return launch_mx4_tiled(c.id, a, s);
   // output columns of a workgroup: an equal share of the rounds that the row blocks need, in

@@ -1,6 +1,6 @@
 """Errors that PyTorch raises inside a call of the C++ module keep their types: a caller that frees
-memory on torch.OutOfMemoryError and tries again does so for these operators too.  Host-only, on the
-runtime of test_current_device."""
+memory on torch.OutOfMemoryError and tries again does so for these operators too.  And grids that the
+runtime would refuse are not asked for.  Host-only, on the runtime of test_current_device."""
 import json
 import os
 import subprocess
@@ -17,3 +17,18 @@ def test_out_of_memory(runtime):  # noqa: F811
     assert set(got) == {"gemm_mxfp4", "gated_mxfp4", "gemm"}
     for name, types in got.items():
         assert types[0] == "OutOfMemoryError", (name, types)
+
+
+def test_grids_are_launchable(runtime):  # noqa: F811
+    """HIP launches fewer than 2^32 threads along a dimension.  No outputs that fit 288 GB need more
+    (bf16: 2^37, MXFP4 of the gated product: 2^39); past that a call returns an error."""
+    r = subprocess.run([sys.executable, os.path.join(HERE, "two_gpus.py"), runtime, "grids"], capture_output=True,
+                       text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+    got = json.loads(r.stdout.strip().splitlines()[-1])
+    assert len(got) == 8
+    for outputs, status, threads in got:
+        if outputs <= 1 << 38:
+            assert status == 0 and len(threads) == 1 and threads[0] < 1 << 32, (outputs, status, threads)
+        else:
+            assert status != 0 and not threads, (outputs, status, threads)

@@ -100,10 +100,28 @@ def out_of_memory():
     print(json.dumps(got))
 
 
+def grids():
+    """The largest products that the documented limits and the card's memory allow, and beyond: their
+    status and the threads of the grid in x, from the C calls with addresses that nothing reads."""
+    at = [ctypes.c_void_p((i + 1) << 44) for i in range(8)]
+    got = []
+    for m, f, k in ((1 << 21, 1 << 17, 128), (1 << 18, 1 << 20, 128), (1 << 20, 1 << 18, 4096), (1 << 21, 1 << 20, 128)):
+        runtime.fake_clear()
+        status = sp.lib.sp24_gated_mxfp4(m, f, k, *at[:4], None, at[4], at[5], None)
+        got.append([m * f, status, [l.grid[0] * l.block[0] for l in runtime.fake_launches()[:runtime.fake_count()]]])
+    for m, n, k in ((1 << 18, 1 << 19, 128), (1 << 21, 1 << 16, 128), (1 << 16, 1 << 21, 256), (1 << 21, 1 << 21, 128)):
+        runtime.fake_clear()
+        status = sp.lib.sp24_gemm_mxfp4(m, n, k, *at[:5], None)
+        got.append([m * n, status, [l.grid[0] * l.block[0] for l in runtime.fake_launches()[:runtime.fake_count()]]])
+    print(json.dumps(got))
+
+
 def main():
     torch.cuda.set_device(0)
     if sys.argv[2] == "out_of_memory":
         return out_of_memory()
+    if sys.argv[2] == "grids":
+        return grids()
     got = {}
     for name, call in globals()[sys.argv[2]]().items():
         runtime.fake_clear()
