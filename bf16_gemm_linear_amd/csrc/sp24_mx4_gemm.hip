@@ -87,10 +87,12 @@ bool can_run(const Mx4Config& c, const Mx4Args& a) {
 }
 
 // SP24_MX4="stream,row blocks", "wave,configuration" or "tiled,configuration" takes that
-// configuration where it can run the call (tuning and tests only).
-const Mx4Config* forced(const Mx4Args& a, const char* v) {
+// configuration where it can run the call; with a "!" after it, it and no other: a call that it
+// cannot run fails (tuning and tests only).
+const Mx4Config* forced(const Mx4Args& a, const char* v, bool* only) {
   char name[8];
   int id;
+  *only = v[strlen(v) - 1] == '!';
   if (sscanf(v, "%7[a-z],%d", name, &id) != 2) return nullptr;
   const Kernel k = strcmp(name, "stream") == 0 ? STREAM : strcmp(name, "wave") == 0 ? WAVE : TILED;
   if (k == TILED && strcmp(name, "tiled") != 0) return nullptr;
@@ -101,8 +103,11 @@ const Mx4Config* forced(const Mx4Args& a, const char* v) {
 
 const Mx4Config* plan(const Mx4Args& a) {
   const char* v = getenv("SP24_MX4");
-  if (v != nullptr && v[0] != '\0')
-    if (const Mx4Config* c = forced(a, v)) return c;
+  if (v != nullptr && v[0] != '\0') {
+    bool only;
+    const Mx4Config* const c = forced(a, v, &only);
+    if (c != nullptr || only) return c;
+  }
   const Mx4Config* best = nullptr;
   double least = 0;
   const int64_t steps = ceil_shift(a.k, kLogStep);
@@ -127,7 +132,7 @@ const Mx4Config* plan(const Mx4Args& a) {
 
 hipError_t launch_mx4_gemm(const Mx4Args& a, hipStream_t s) {
   const Mx4Config* const best = plan(a);
-  if (best == nullptr) return hipErrorInvalidConfiguration;  // more outputs than the card's memory holds
+  if (best == nullptr) return hipErrorInvalidConfiguration;  // more outputs than any memory holds, or the override
   const Mx4Config& c = *best;
   if (c.kernel == WAVE) return launch_mx4_wave(c.id, a, s);
   if (c.kernel == TILED) return launch_mx4_tiled(c.id, a, s);

@@ -116,12 +116,33 @@ def grids():
     print(json.dumps(got))
 
 
+def configurations():
+    """SP24_MX4 by name: status and number of launches of a product, a gated product and one to MXFP4, of
+    the tokens given, from the C calls with addresses that nothing reads."""
+    at = [ctypes.c_void_p((i + 1) << 44) for i in range(8)]
+    got = {}
+    for config, m in (("stream,8", 17), ("stream,8!", 16), ("stream,8!", 17), ("stream,1!", 8), ("stream,2!", 64),
+                      ("stream,2!", 65), ("wave,4!", 8), ("wave,5!", 8), ("tiled,3!", 8), ("tiled,4!", 8),
+                      ("wave,9!", 8), ("walk,1!", 8), ("!", 8)):
+        os.environ["SP24_MX4"] = config
+        got["%s %d" % (config, m)] = calls = []
+        for call in (lambda: sp.lib.sp24_gemm_mxfp4(m, 512, 256, *at[:5], None),
+                     lambda: sp.lib.sp24_gated_mxfp4(m, 256, 256, *at[:5], None, None, None),
+                     lambda: sp.lib.sp24_gated_mxfp4(m, 256, 256, *at[:4], None, at[4], at[5], None)):
+            runtime.fake_clear()
+            status = call()
+            calls.append([status, runtime.fake_count()])
+    print(json.dumps(got))
+
+
 def main():
     torch.cuda.set_device(0)
     if sys.argv[2] == "out_of_memory":
         return out_of_memory()
     if sys.argv[2] == "grids":
         return grids()
+    if sys.argv[2] == "configurations":
+        return configurations()
     got = {}
     for name, call in globals()[sys.argv[2]]().items():
         runtime.fake_clear()
