@@ -768,7 +768,7 @@ def dense_gemm(x, w, x_scale=None, w_scale=None, out=None, ws=None):
     return _gemm(False, x, w, None, x_scale, w_scale, out, ws)
 
 
-# --------------------------------------------------------------------------- probes
+# --------------------------------------------------------------------------- MXFP4 and norm
 
 def ffn_mxfp4_workspace_size(m: int, d: int, f: int) -> int:
     """Workspace bytes of ffn_mxfp4 for m tokens."""
@@ -796,6 +796,8 @@ gated_mxfp4 = _from_native("gated_mxfp4")
 rmsnorm = _from_native("rmsnorm")
 ffn_mxfp4 = _from_native("ffn_mxfp4")
 
+
+# --------------------------------------------------------------------------- probes
 
 def probe_mfma_layout(variant: int, a: torch.Tensor, b: torch.Tensor, idx: torch.Tensor,
                       c: torch.Tensor, n_exp: int):

@@ -12,12 +12,13 @@
 // fits' errors are 4 to 9% rms.  On 980 shapes kept out of a fit the picks took 1.6% longer than
 // the best configuration measured, 11% at the 95th percentile (of all: 1.0% from 1025 tokens, 1.3%
 // to 16, 2.8% from 65 to 256); with a, b and c alone it was 2.7%.
-// What the numbers say: few tokens go to the stream kernel, whose waves walk K apart and pull W at
-// the rate of memory; long K over few tiles to the wave kernel (m = 256, 4096 x 14336: 16.2 us
-// against 21 on tiles); short K and many tiles to the tiled one (m = 1024, 14336 x 4096: 36.8
-// against 65), on 128 x 128 tiles until rounds of 256 x 256 are many or well filled (5000 x 4096 x
-// 4096: 50.8 us against 60.9; 6000 x 8192 x 8192: 224 against 196).
-// Measured and not built: splitting K over workgroups with a reduction (gained at one shape of
+// What the numbers say (HIP graphs): few tokens go to the stream kernel, whose waves walk K apart and
+// pull W at the rate of memory; long K over few tiles to the wave kernel (m = 256, 4096 x 14336: 16.2 us
+// against 23.2 on tiles); short K and many tiles to the tiled one (m = 1024, 14336 x 4096: 35.9 against
+// 62.8), on 128 x 128 tiles until rounds of 256 x 256 are many or well filled (5000 x 4096 x 4096: 55.2
+// us against 61.3; 6000 x 8192 x 8192: 238 against 197).  Near a balance the cards differ (gated 2047 x
+// 14336 x 4096: 128 x 128 7 to 10% ahead on one, 3% behind on another).
+// Measured and not built: splitting K of the tiled kernel over workgroups with a reduction (gained at one shape of
 // fifty, n = 512, k = 8192), and a call's columns in two launches, whole rounds of large tiles and
 // the rest on small ones (slower or equal at 12 of 14 shapes).
 #include <stdio.h>
@@ -137,7 +138,8 @@ hipError_t launch_mx4_gemm(const Mx4Args& a, hipStream_t s) {
   if (c.kernel == WAVE) return launch_mx4_wave(c.id, a, s);
   if (c.kernel == TILED) return launch_mx4_tiled(c.id, a, s);
   // output columns of a workgroup: an equal share of the rounds that the row blocks need, in
-  // fours (n = 14336: 56 columns on every CU 7.35 us, 64 on most of them 7.62)
+  // fours (n = 14336, k = 4096 in HIP graphs: 56 columns on every CU 7.41 us, 64 on most of them 7.54;
+  // 16 tokens 7.42 and 7.62)
   const int most = a.gated ? 8 * c.id : 16 * c.id;
   const int64_t rounds = ceil_div(ceil_div(a.n, most), kCus);
   int rows = (int)ceil_div(ceil_div(a.n, rounds * kCus), 4) * 4;

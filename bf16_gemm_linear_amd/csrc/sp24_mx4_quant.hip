@@ -2,8 +2,8 @@
 // [-127, 127] (0 for a block of zeros), codes e2m1_rne(clamp(x 2^-e, +-6)), scale byte
 // e + 127; a block with an Inf or NaN gets byte 255 and codes 0.
 //
-// Memory-bound: 2 + 0.53 bytes a value.  28672 x 8192 takes 103 us, 5.8 TB/s, and 118 us back,
-// 5.1 TB/s, the rate of a large copy (82 with the codes in the last-level cache); 16 x 14336
+// Memory-bound: 2 + 0.53 bytes a value.  28672 x 8192 takes 103 us, 5.8 TB/s, and 118 to 121 us back,
+// 5.0 TB/s, the rate of a large copy (82 with the codes in the last-level cache); 16 x 14336
 // takes 2.1 and 1.9 us, of which 1.7 are any launch's.
 // A lane takes 8 values (a 16-byte load, a 4-byte store), 4 lanes a block, 16 lanes a word of
 // scales.  Non-temporal loads of bf16 and stores of either form: 118 and 119 us without.

@@ -9,9 +9,9 @@
 // a wave's chain of waits is 1 / KW of the steps.  The waves' sums are joined through LDS
 // in a fixed order.  W is read once, with the non-temporal hint; X comes from L2.
 //
-// Measured: one token 14336 x 4096 6.5 us (4.8 TB/s; the best of the other kernels 7.1), gated
-// 11.9 (5.2 TB/s, three weights in turn partly from the last-level cache); 16 tokens gated
-// 14336 x 4096 with MXFP4 output 12.7 and 4096 x 14336 7.5.  Bound by memory and by the first
+// Measured, calls in a row: one token 14336 x 4096 6.5 us (4.8 TB/s), gated 11.9 (5.2 TB/s, three
+// weights in turn partly from the last-level cache); in HIP graphs one token 7.1 (the best of the
+// other kernels 7.4), 16 tokens gated 14336 x 4096 with MXFP4 output 12.7 and 4096 x 14336 7.5 (9.8).  Bound by memory and by the first
 // loads' latency; with W loaded straight into registers, less of it in flight, one token
 // 14336 x 4096 took 9.2 (the rings, at first: 7.4).
 //

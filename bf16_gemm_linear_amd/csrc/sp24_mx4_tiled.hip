@@ -19,9 +19,10 @@
 // LDS rows of 128 bytes are XOR-swizzled in 16-byte pieces; the swizzle is applied on
 // the global side, since a load writes lane i's bytes to slot i.
 //
-// Measured: 8192 x 28672 x 8192 869 to 900 us (4.4 PFLOP/s) on 256 x 256, 1095 on 128 x 128: bound by
-// power (1.6 GHz under load; the matrix instructions alone take 600 us, the loads alone 545).
-// Gated 2047 x 14336 x 4096 132 to 138 us.  In one round of 256 x 256 tiles a step takes 0.9 us,
+// Measured: 8192 x 28672 x 8192 869 to 935 us over the cards (4.1 to 4.4 PFLOP/s) on 256 x 256, 1095
+// to 1126 on 128 x 128: bound by power (1.6 GHz under load; the matrix instructions alone take 600 us,
+// the loads alone 545) and by what each round's start and outputs leave idle.
+// Gated 2047 x 14336 x 4096 132 to 148 us (128 x 128: 152 beside 148).  In one round of 256 x 256 tiles a step takes 0.9 us,
 // near the instructions' own rate, and the start and the outputs' 32 MB 10 us.  Outputs go through
 // LDS into whole rows: straight from the registers, half lines of many rows, 2048 x 32768 x 4096
 // took 177 us against 164.

@@ -10,8 +10,8 @@
 // the end, and the loads of KW waves are in flight all the time.  The waves' sums are joined
 // through LDS in a fixed order, a part of the tile at a time.
 //
-// Measured, against the best tiled configuration: 4096 x 14336 with 200 tokens 15.5 us (22.8) and
-// with 1000 38 (43.7; 3.1 PFLOP/s), 128 x 4096 x 4096 5.7 (8.6); 77 x 4096 x 14336 10.9.  Bound by
+// Measured in HIP graphs, against the best tiled configuration: 4096 x 14336 with 77 tokens 11.1 us
+// (22.6), with 200 15.0 (23.0) and with 1000 39.3 (44.5; 3.0 PFLOP/s), 128 x 4096 x 4096 5.4 (8.5).  Bound by
 // what a CU takes in from L2: at 77 tokens 0.7 MB, 5 us at 64 bytes a cycle, beside the weight's 6.
 //
 // Operands: for E2M1 codes lane l of v_mfma_scale_f32_32x32x64_f8f6f4 holds row l % 32 and

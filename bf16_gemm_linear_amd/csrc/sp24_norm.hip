@@ -3,11 +3,12 @@
 // v = t rstd w with rstd = 1 / sqrt(mean(t^2) + eps).
 //
 // Memory-bound: 2 bytes read a value (6 moved with a residual) and 1 written (E4M3, INT8).
-// 8191 x 8192 with a residual takes 81 us to E4M3 with a scale per row, 83 with one per group
-// of 128 and 77 to MXFP4, 5.7 TB/s (a large copy: 5.1); the outputs' non-temporal hint is worth
+// 8191 x 8192 with a residual takes 78 to 81 us to E4M3 with a scale per row, 81 with one per group
+// of 128, 74 to 76 to MXFP4 and 91 to bf16, 5.8 TB/s (a large copy: 5.1); the outputs' non-temporal hint is worth
 // a quarter of it where the inputs come from the last-level cache (68 us, 89 without).  Few rows
 // are bound by a thread's chain of instructions: reductions over lanes go by register exchanges
-// (through LDS: 1 x 4096 to E4M3 3.1 us, per group 4.1; now 2.5 and 2.6, 1.7 any launch's).
+// (through LDS: 1 x 4096 with a residual to E4M3 3.1 us, per group 4.1; now 2.7 and 3.0, 1.7 any
+// launch's).
 // One pass: a row stays in registers as fp32 from the loads to the codes, T threads a row
 // with NV vectors of 8 values each.  The codes do not wait for rstd: with u = t w, a scale
 // is s = max|u| rstd / top, so v / s = u (top / max|u|), and one reduction over the row
@@ -320,11 +321,12 @@ hipError_t launch_norm_tn(const NormArgs& a, hipStream_t s) {
 }
 
 // Threads a row: one vector a thread for short and few rows (to 4096 values, 2^21 in all), where
-// the chain of a thread is the time (E4M3, no residual, us: 16 x 2048 on 256 x 1 and 64 x 4 2.4 and
-// 3.2, 256 x 4096 on 512 x 1 and 256 x 2 2.8 and 3.1; with more rows it turns round, 1000 x 4096 5.3
-// and 5.0, 8191 x 4096 23.5 and 19.5).  Else a wave to 2048 values, then one workgroup with two
-// vectors a thread (8191 x 8192 E4M3 per group of 128 and residual on 512 x 2 83, on 1024 x 1 85;
-// 16 rows of 8192 3.3 and 3.5), four to 32768 (2048 x 20480 38, on 1024 x 8 51) and eight beyond.
+// the chain of a thread is the time (E4M3, no residual, us: 16 x 2048 on 256 x 1 and 64 x 4 2.7 and
+// 3.5, 256 x 4096 on 512 x 1 and 256 x 2 3.0 and 3.2; with more rows it turns round, 1000 x 4096 4.9
+// and 4.5, 8191 x 4096 25.0 and 20.4).  Else a wave to 2048 values, then one workgroup with two
+// vectors a thread (8191 x 8192 E4M3 per group of 128 and residual on 512 x 2 81, on 1024 x 1 84;
+// 16 rows of 8192 3.3 and 3.4), four to 32768 (2048 x 20480 36, on 1024 x 8 52; the lanes past the
+// row idle) and eight beyond.
 template <int KIND>
 hipError_t launch_norm_kind(const NormArgs& a, hipStream_t s) {
   const int64_t nv = a.k / 8;

@@ -8,7 +8,8 @@ this library's: per layer one `ffn_mxfp4` (RMS norm with residual addition and M
 product with MXFP4 output, down product), the residual carried in place, and at the end `rmsnorm`
 in bf16.  The same stack in bf16 with PyTorch's own operators runs beside it.  Prints one JSON
 object: milliseconds of each, weight bytes, and the relative error of MXFP4 against bf16 (what 4-bit
-weights and activations cost on random data, not an error of the kernels).
+weights and activations cost on random data, layer after layer, not an error of the kernels: those
+agree with the same blocks in float64 on the same 4-bit values).
 """
 from __future__ import annotations
 

@@ -487,8 +487,10 @@ int sp24_dequant_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t rows
 /* Y = X . W^T of two MXFP4 operands; fp32 accumulation, bf16 output.
  *   x_codes [m, k/2], x_scales m*k/32 bytes; w_codes [n, k/2], w_scales n*k/32
  *   bytes; y_bf16 [m, n].
- * Requires m, n >= 1, at most 2^21; 128 <= k <= 2^24, k % 128 == 0.  The sum over k is formed in a fixed order for a given (m, n, k): results
- * are bitwise reproducible.  No workspace. */
+ * Requires m, n >= 1, at most 2^21; 128 <= k <= 2^24, k % 128 == 0.  The sum over k
+ * is formed in a fixed order for a given (m, n, k): results are bitwise
+ * reproducible.  No workspace.  (SP24_ERR_HIP where no grid covers the outputs:
+ * beyond 2^39 of them.) */
 int sp24_gemm_mxfp4(int64_t m, int64_t n, int64_t k, const uint8_t* x_codes, const uint8_t* x_scales,
                     const uint8_t* w_codes, const uint8_t* w_scales, void* y_bf16, void* stream);
 
@@ -525,7 +527,9 @@ typedef enum sp24_norm_kind {
  *     finite gets s = NaN and codes 0;
  *   SP24_NORM_MXFP4: the blocks of v as sp24_quant_mxfp4 rounds them.
  * All of it in fp32 from the unrounded t; v is never rounded to bf16 in between,
- * so codes can differ by a rounding from those of a norm and a quantiser in turn.
+ * so codes can differ by a rounding from those of a norm and a quantiser in turn;
+ * and where v / s lies within an fp32 rounding (2^-24 of it) of the middle between
+ * two codes, either of them is given.  v has to be in fp32's range, t * w need not.
  *   x_bf16 [m, k]; residual_bf16 [m, k] or NULL; residual_out_bf16 [m, k], given
  *   exactly when residual is (it may be the same buffer: an update in place);
  *   weight_bf16 [k]; eps > 0 and finite (SP24_ERR_MODE otherwise).
@@ -537,8 +541,8 @@ int sp24_rmsnorm(int kind, int64_t m, int64_t k, int64_t group, const void* x_bf
                  void* residual_out_bf16, const void* weight_bf16, float eps, void* out, void* scales_out,
                  void* stream);
 
-/* A pre-norm feed-forward block in MXFP4, three launches: X + residual normed into MXFP4 (sp24_rmsnorm), the gated
- * projection with an MXFP4 output (sp24_gated_mxfp4), the down-projection
+/* A pre-norm feed-forward block in MXFP4, three launches: X + residual normed into
+ * MXFP4 (sp24_rmsnorm), the gated projection with an MXFP4 output (sp24_gated_mxfp4), the down-projection
  * (sp24_gemm_mxfp4); bit for bit those calls in turn.
  *   x_bf16, residual_bf16 (or NULL), residual_out_bf16, weight_bf16 [d], eps as
  *   sp24_rmsnorm; gu_codes [2f, d/2] and gu_scales as sp24_gated_mxfp4; down_codes
