@@ -16,8 +16,9 @@
 // same time).  Where a maximum of |u| has left fp32's range, or comes so near its lower end
 // that values would lose bits (very large or small weights), v itself may be in range: such a
 // row takes the maxima of |t rstd w| in a second reduction.  For that t stays in the registers,
-// and t w is formed twice: 1 to 4% of a call to 32768 values, 11% beyond, where the weight is
-// loaded again (1024 x 65536 to E4M3 49 us from 44).  Sums are fp32 in a fixed order.
+// and t w is formed twice: up to 4% of a call (7% with groups of several waves: 8191 x 8192 per
+// group of 1024 50 us from 46.5), 10% past 32768 values, where the weight is loaded again (1024 x
+// 65536 to E4M3 49 us from 44).  Sums are fp32 in a fixed order.
 #include "sp24_fp8.hpp"
 #include "sp24_mx4.hpp"
 
@@ -171,7 +172,33 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rmsnorm_kernel(
 
   ss = __uint_as_float(fold_wave(__float_as_uint(ss), bits_sum));
   if constexpr (ROWS) key = fold_wave(key, bits_max);
-  if constexpr (GROUPS) key = __any(off) ? 1u : 0u;
+  auto weight = [&](int j) {
+    if constexpr (KEEP_W) {
+      return wd[j];
+    } else {
+      const int i = tl + j * T;
+      return i < nv ? reinterpret_cast<const u32x4*>(w)[i] : u32x4{0u, 0u, 0u, 0u};
+    }
+  };
+  if constexpr (GROUPS) {
+    if (__any(off)) {
+      // groups of true zeros (channels without a signal) are in range, or they would cost their
+      // rows a second reduction, 10% of 8191 x 8192; zeros of values that are not are out of it
+      off = false;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        if (tl + j * T >= nv) continue;
+        if (gkey[j] != 0) {
+          off = off || out_of_range(gkey[j]);
+        } else {
+          const u32x4 wj = weight(j);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) off = off || (u[j][e] != 0.0f && bf16_of(wj, e) != 0.0f);
+        }
+      }
+    }
+    key = __any(off) ? 1u : 0u;
+  }
   if constexpr (NW > 1) {
     if (lane == 0) {
       sh_sum[threadIdx.x / 64] = ss;
@@ -191,15 +218,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rmsnorm_kernel(
   }
   const float rstd = 1.0f / __builtin_sqrtf(ss / (float)k + eps);
 
-  auto weight = [&](int j) {
-    if constexpr (KEEP_W) {
-      return wd[j];
-    } else {
-      const int i = tl + j * T;
-      return i < nv ? reinterpret_cast<const u32x4*>(w)[i] : u32x4{0u, 0u, 0u, 0u};
-    }
-  };
-  bool again = false;  // this row's maxima are those of |t rstd w|
+  bool again = false;  // u is t rstd in this row, and its maxima are those of |t rstd w|
   if constexpr (ROWS || GROUPS) {
     auto bad = [&](uint32_t row_key) { return GROUPS ? row_key != 0 : out_of_range(row_key); };
     again = nv > 0 && bad(key);
@@ -220,10 +239,16 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rmsnorm_kernel(
       const u32x4 wj = weight(j);
       uint32_t mk = 0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) mk = max(mk, __float_as_uint(u[j][e] * rstd * bf16_of(wj, e)) & 0x7FFFFFFFu);
+      for (int e = 0; e < 8; ++e) mk = max(mk, __float_as_uint(u[j][e] * bf16_of(wj, e)) & 0x7FFFFFFFu);
       return mk;
     };
     if (any_again) {
+      if (again) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) u[j][e] *= rstd;
+      }
       if constexpr (ROWS) {
         uint32_t mk = 0;
 #pragma unroll
@@ -256,12 +281,10 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rmsnorm_kernel(
     }
   }
 
-  // v = (t pre) w post: where the maxima are of |t w|, rstd goes to the scale alone
-  const bool in_scale = (ROWS || GROUPS) && !again;
-  const float pre = in_scale ? 1.0f : rstd, post = in_scale ? rstd : 1.0f;
+  const float left = again ? 1.0f : rstd;  // what the 8-bit forms' scales still have to take
   NormDiv d{0.0f, 0.0f, 1.0f, false};
   if constexpr (ROWS) {
-    const float s = norm_scale<KIND>(key, post, d);
+    const float s = norm_scale<KIND>(key, left, d);
     if (tl == 0 && nv > 0) static_cast<float*>(scales)[row] = s;
   }
   u32x4 wnext = weight(0);
@@ -271,7 +294,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rmsnorm_kernel(
     const u32x4 wj = wnext;
     if (j + 1 < NV) wnext = weight(j + 1);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) u[j][e] = u[j][e] * pre * bf16_of(wj, e);
+    for (int e = 0; e < 8; ++e) u[j][e] = (ROWS || GROUPS ? u[j][e] : u[j][e] * rstd) * bf16_of(wj, e);
     if constexpr (KIND == SP24_NORM_BF16) {
       if (i < nv) {
         u32x4 o;
@@ -293,7 +316,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rmsnorm_kernel(
       if (i < nv) {
         if constexpr (GROUPS) {
           const int g = group_of(i);
-          const float s = norm_scale<KIND>(in_lds ? gmax[rl * ng + g] : gkey[j], post, d);
+          const float s = norm_scale<KIND>(in_lds ? gmax[rl * ng + g] : gkey[j], left, d);
           if (i == g * vpg) static_cast<float*>(scales)[(size_t)row * ng + g] = s;
         }
         __builtin_nontemporal_store(norm_codes8<KIND>(u[j], d), static_cast<u32x2*>(out) + base + i);

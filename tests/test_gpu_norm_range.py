@@ -96,3 +96,30 @@ def test_one_group_out_of_range():
         o, s, _ = sp.rmsnorm(x.to(DEV), w.to(DEV), sp.NORM_FP8_GROUPS, eps=1e-30, group=group)
         torch.cuda.synchronize()
         by_kind(sp, sp.NORM_FP8_GROUPS, o, s, v, group)
+
+
+@pytest.mark.parametrize("k,group", [(512, 64), (384, 192), (2048, 128), (8192, 1024), (4608, 1536), (40960, 512)])
+def test_groups_of_zeros(k, group):
+    """A group of zeros (of x, of the weight, of one lane's values) gets scale 1 and codes 0, the row's other
+    groups what they get without it: their codes do not depend on the sum of squares."""
+    sp = need_sp()
+    x, w = W.randn_bf16((4, k), k).float(), 1 + 0.2 * W.randn_bf16((k,), 3).float()
+    x[1, group:2 * group] = 0.0
+    x[2, group:group + 8] = 0.0
+    x[3] = 0.0
+    x = x.to(torch.bfloat16)
+    for zero in (False, True):
+        if zero:
+            w[:group] = 0.0
+        wb = w.to(torch.bfloat16)
+        v, _ = R.norm_ref(W.bf16_bits(x), None, W.bf16_bits(wb), 1e-5)
+        announce("rmsnorm zeros", k, group, zero)
+        o, s, _ = sp.rmsnorm(x.to(DEV), wb.to(DEV), sp.NORM_FP8_GROUPS, eps=1e-5, group=group)
+        torch.cuda.synchronize()
+        by_kind(sp, sp.NORM_FP8_GROUPS, o, s, v, group)
+        assert (s[1, 1] == 1).item() and (s[3] == 1).all().item() and not o.view(torch.uint8)[1, group:2 * group].any().item()
+        y = x.clone()
+        y[1, group:2 * group] = 1.0
+        o2, _, _ = sp.rmsnorm(y.to(DEV), wb.to(DEV), sp.NORM_FP8_GROUPS, eps=1e-5, group=group)
+        torch.cuda.synchronize()
+        assert torch.equal(o.view(torch.uint8)[1, 2 * group:], o2.view(torch.uint8)[1, 2 * group:])
