@@ -1,8 +1,8 @@
 """Python binding of libsp24: 2:4 structured-sparse GEMM for gfx950 (MI355X).
 
-Thin marshalling over the C ABI declared in include/sp24.h (ctypes; the MXFP4
-operators and the norm, whose kernels are shorter than a call through ctypes, in
-the C++ module _sp24): every call checks dtypes, devices, shapes and contiguity
+Thin marshalling over the C ABI declared in include/sp24.h (ctypes; the MXFP4 and
+integer 4-bit operators, the norm, the router and the experts, whose kernels are
+shorter than a call through ctypes, in the C++ module _sp24): every call checks dtypes, devices, shapes and contiguity
 of torch tensors, passes their device pointers and the current HIP stream, and
 raises on a non-OK status.
 PyTorch is used only for device memory and streams; all arithmetic runs in the
@@ -35,6 +35,8 @@ __all__ = [
     "prune_compress", "decompress", "quant_fp8", "gemm", "dense_gemm", "workspace_size", "plan",
     "quant_mxfp4", "dequant_mxfp4", "gemm_mxfp4", "gated_mxfp4", "rmsnorm", "ffn_mxfp4", "ffn_mxfp4_workspace_size",
     "mxfp4_scale_index", "NORM_BF16", "NORM_FP8_ROWS", "NORM_INT8_ROWS", "NORM_FP8_GROUPS", "NORM_MXFP4",
+    "quant_int4", "dequant_int4", "gemm_int4", "pack_int4", "unpack_int4", "route", "ROUTE_SOFTMAX", "ROUTE_SIGMOID",
+    "experts_int4", "experts_int4_workspace_size",
     "probe_mfma_layout", "probe_mfma_rate", "probe_copy", "probe_read", "probe_ring",
 ]
 
@@ -44,6 +46,7 @@ OP_GEMM, OP_QUANT, OP_DENSE_GEMM, OP_GEMM_QX, OP_PALETTE_ANALYZE, OP_PALETTE_GEM
 OP_GEMM_ROWS_QX = 6
 OP_GEMM_GROUPS = 7
 NORM_BF16, NORM_FP8_ROWS, NORM_INT8_ROWS, NORM_FP8_GROUPS, NORM_MXFP4 = 0, 1, 2, 3, 4
+ROUTE_SOFTMAX, ROUTE_SIGMOID = 0, 1
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 lib_path = os.path.join(_HERE, "libsp24.so")
@@ -61,6 +64,18 @@ class _PaletteStruct(ctypes.Structure):
     """sp24_palette_weight (include/sp24.h)."""
     _fields_ = [("palette", _vp), ("n_pal", _i64), ("sm", _vp), ("ix", _vp), ("pal_rows", _vp),
                 ("n_verb", _i64), ("verb", _vp), ("verb_rows", _vp)]
+
+
+class _RouterStruct(ctypes.Structure):
+    """sp24_router (include/sp24.h)."""
+    _fields_ = [("kind", _int), ("logits_fp32", _int), ("experts", _i64), ("top", _i64), ("groups", _i64),
+                ("top_groups", _i64), ("group_best", _int), ("renormalise", _int), ("factor", ctypes.c_float)]
+
+
+class _ExpertsStruct(ctypes.Structure):
+    """sp24_int4_experts (include/sp24.h)."""
+    _fields_ = [("experts", _i64), ("d", _i64), ("f", _i64), ("group", _i64), ("gu_codes", _vp), ("gu_scales", _vp),
+                ("gu_zeros", _vp), ("down_codes", _vp), ("down_scales", _vp), ("down_zeros", _vp)]
 
 
 class Plan(ctypes.Structure):
@@ -105,6 +120,12 @@ _SIGS = {
     "sp24_rmsnorm": [_int, _i64, _i64, _i64, _vp, _vp, _vp, _vp, ctypes.c_float, _vp, _vp, _vp],
     "sp24_ffn_mxfp4": [_i64, _i64, _i64, _vp, _vp, _vp, _vp, ctypes.c_float, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
     "sp24_ffn_mxfp4_workspace_size": [_i64, _i64, _i64],
+    "sp24_quant_int4": [_vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp],
+    "sp24_dequant_int4": [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp],
+    "sp24_gemm_int4": [_i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp],
+    "sp24_route": [ctypes.POINTER(_RouterStruct), _i64, _vp, _vp, _vp, _vp, _vp],
+    "sp24_experts_int4": [ctypes.POINTER(_ExpertsStruct), _i64, _i64, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
+    "sp24_experts_int4_workspace_size": [_i64, _i64, _i64, _i64, _i64],
     "sp24_status_string": [_int],
     "sp24_version": [],
     "sp24_probe_mfma_layout": [_int, _vp, _vp, _vp, _vp, _int, _vp],
@@ -124,10 +145,11 @@ for _name, _args in _SIGS.items():
     _f.restype = _int
 lib.sp24_workspace_size.restype = _sz
 lib.sp24_ffn_mxfp4_workspace_size.restype = _sz
+lib.sp24_experts_int4_workspace_size.restype = _sz
 lib.sp24_status_string.restype = ctypes.c_char_p
 
 
-try:  # the binding of the MXFP4 operators and the norm, in C++ (csrc/sp24_python.cpp)
+try:  # the binding of the MXFP4 and integer 4-bit operators, the norm and the router, in C++ (csrc/sp24_python.cpp)
     from . import _sp24 as _native
     _built = getattr(_native, "torch_version", "another")
     if _built != re.match(r"\d+(\.\d+)*", str(torch.__version__)).group():
@@ -795,6 +817,42 @@ gemm_mxfp4 = _from_native("gemm_mxfp4")
 gated_mxfp4 = _from_native("gated_mxfp4")
 rmsnorm = _from_native("rmsnorm")
 ffn_mxfp4 = _from_native("ffn_mxfp4")
+
+
+# --------------------------------------------------------------------------- integer 4-bit weights, experts
+
+_INT4_PLACES = (0, 2, 4, 6, 1, 3, 5, 7)  # which of eight values each four bits of a word hold, lowest first
+
+
+def pack_int4(q: torch.Tensor) -> torch.Tensor:
+    """Codes as numbers 0..15 (uint8 [..., cols], cols % 8 == 0, on any device) -> the bytes [..., cols/2]
+    that gemm_int4 and experts_int4 read (a load-time helper)."""
+    if q.dtype != torch.uint8 or q.dim() < 1 or q.shape[-1] % 8:
+        raise ValueError("codes must be uint8 with a multiple of 8 columns")
+    b = q.reshape(*q.shape[:-1], -1, 8)[..., list(_INT4_PLACES)]
+    return ((b[..., 0::2] & 15) | (b[..., 1::2] << 4)).reshape(*q.shape[:-1], -1)
+
+
+def unpack_int4(codes: torch.Tensor) -> torch.Tensor:
+    """The inverse of pack_int4: bytes [..., cols/2] -> numbers 0..15 (uint8 [..., cols])."""
+    if codes.dtype != torch.uint8 or codes.dim() < 1 or codes.shape[-1] % 4:
+        raise ValueError("codes must be uint8 with a multiple of 4 bytes a row")
+    c = codes.reshape(*codes.shape[:-1], -1, 4)
+    p = torch.stack((c & 15, c >> 4), -1).reshape(*c.shape[:-1], 8)
+    return p[..., [_INT4_PLACES.index(j) for j in range(8)]].reshape(*codes.shape[:-1], -1)
+
+
+def experts_int4_workspace_size(tokens: int, d: int, f: int, experts: int, top: int) -> int:
+    """Workspace bytes of experts_int4 for that many tokens."""
+    return int(lib.sp24_experts_int4_workspace_size(tokens, d, f, experts, top))
+
+
+# as the C++ module has them (help() shows their arguments)
+quant_int4 = _from_native("quant_int4")
+dequant_int4 = _from_native("dequant_int4")
+gemm_int4 = _from_native("gemm_int4")
+route = _from_native("route")
+experts_int4 = _from_native("experts_int4")
 
 
 # --------------------------------------------------------------------------- probes

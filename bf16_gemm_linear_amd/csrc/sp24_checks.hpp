@@ -18,6 +18,27 @@ inline bool overlaps(const void* a, size_t abytes, const void* b, size_t bbytes)
   return a0 < b0 + bbytes && b0 < a0 + abytes;
 }
 
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+
+// every output against every input and every other output (NULL spans are skipped)
+template <int NI, int NO>
+bool any_alias(const Span (&in)[NI], const Span (&out)[NO]) {
+  for (int o = 0; o < NO; ++o) {
+    if (out[o].p == nullptr || out[o].bytes == 0) continue;
+    for (int i = 0; i < NI; ++i)
+      if (in[i].p != nullptr && overlaps(out[o].p, out[o].bytes, in[i].p, in[i].bytes)) return true;
+    for (int j = o + 1; j < NO; ++j)
+      if (out[j].p != nullptr && overlaps(out[o].p, out[o].bytes, out[j].p, out[j].bytes)) return true;
+  }
+  return false;
+}
+
+// Parts of a workspace begin at multiples of 256 bytes.
+inline size_t pad(size_t b) { return (b + 255) / 256 * 256; }
+
 inline bool sync_check_enabled() {
   static const bool on = [] {
     const char* v = getenv("SP24_SYNC_CHECK");

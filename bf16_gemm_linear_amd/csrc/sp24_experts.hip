@@ -1,0 +1,89 @@
+// Around the experts' products: the pairs (token, slot) in the order of their experts before them, and
+// the weighted sum over a token's slots behind them.
+#include "sp24_int4.hpp"
+#include "sp24_mx4.hpp"
+
+namespace sp24 {
+namespace {
+
+constexpr int kSortThreads = 256;
+
+// Workgroup e finds the places of expert e: it counts the ids below e (where its range begins) and lists
+// the pairs with id e, in their order.  A thread takes a run of neighbouring pairs, so the order holds
+// without atomics.
+__global__ __launch_bounds__(kSortThreads) void sort_pairs_kernel(const int32_t* __restrict__ ids, int count,
+                                                                  int experts, int* __restrict__ offsets,
+                                                                  int* __restrict__ order) {
+  __shared__ int sums[kSortThreads / 64][2];
+  const int e = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int run = (count + kSortThreads - 1) / kSortThreads;
+  const int from = min(count, tid * run), to = min(count, from + run);
+  int below = 0, mine = 0;
+  for (int i = from; i < to; ++i) {
+    const int id = ids[i];
+    below += id >= 0 && id < e;
+    mine += id == e;
+  }
+  int upto = mine;
+#pragma unroll
+  for (int o = 1; o < 64; o *= 2) {
+    const int v = __shfl_up(upto, o), b = __shfl_xor(below, o);
+    if (lane >= o) upto += v;
+    below += b;
+  }
+  if (lane == 63) {
+    sums[wave][0] = upto;
+    sums[wave][1] = below;
+  }
+  __syncthreads();
+  int start = 0, before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kSortThreads / 64; ++w) {
+    start += sums[w][1];
+    before += w < wave ? sums[w][0] : 0;
+    all += sums[w][0];
+  }
+  if (tid == 0) {
+    offsets[e] = start;
+    if (e == experts - 1) offsets[experts] = start + all;
+  }
+  int at = start + before + upto - mine;
+  for (int i = from; i < to; ++i)
+    if (ids[i] == e) order[at++] = i;
+}
+
+// y[t] = sum over slots of weight * part, in the order of the slots; 4 columns a thread (d % 32 == 0).
+__global__ __launch_bounds__(256) void join_pairs_kernel(const float* __restrict__ part,
+                                                         const int32_t* __restrict__ ids,
+                                                         const float* __restrict__ weights, int64_t units, int quads,
+                                                         int top, int experts, uint16_t* __restrict__ y) {
+  for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < units; u += (int64_t)gridDim.x * 256) {
+    const int64_t t = u / quads;
+    const int q = (int)(u - t * quads);
+    f32x4 sum{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < top; ++j) {
+      const int64_t p = t * top + j;
+      if ((uint32_t)ids[p] >= (uint32_t)experts) continue;
+      sum += weights[p] * reinterpret_cast<const f32x4*>(part)[p * quads + q];
+    }
+    reinterpret_cast<u32x2*>(y)[u] = u32x2{f32x2_to_bf16x2(sum[0], sum[1]), f32x2_to_bf16x2(sum[2], sum[3])};
+  }
+}
+
+}  // namespace
+
+hipError_t launch_sort_pairs(const int32_t* ids, int64_t count, int experts, int* offsets, int* order, hipStream_t s) {
+  hipLaunchKernelGGL(sort_pairs_kernel, dim3(experts), dim3(kSortThreads), 0, s, ids, (int)count, experts, offsets,
+                     order);
+  return hipGetLastError();
+}
+
+hipError_t launch_join_pairs(const float* part, const int32_t* ids, const float* weights, int64_t tokens, int top,
+                             int experts, int d, uint16_t* y, hipStream_t s) {
+  const int64_t units = tokens * (d / 4), blocks = (units + 255) / 256;
+  hipLaunchKernelGGL(join_pairs_kernel, dim3((uint32_t)(blocks < 65536 ? blocks : 65536)), dim3(256), 0, s, part, ids,
+                     weights, units, d / 4, top, experts, y);
+  return hipGetLastError();
+}
+
+}  // namespace sp24

@@ -1,0 +1,150 @@
+// bf16 <-> integer 4-bit codes with a bf16 scale, and if asked for a zero point, per group of a row.
+//
+//   symmetric:   s = bf16(amax / 7), q = clamp(rne(w / s), -8, 7) + 8
+//   zero points: lo = min(0, min w), hi = max(0, max w), s = bf16((hi - lo) / 15),
+//                z = clamp(rne(-lo / s), 0, 15), q = clamp(rne(w / s) + z, 0, 15)
+// with s = 1 where that is 0, and s = NaN, q = z = 8 for a group with an Inf or a NaN.  The divisions
+// are IEEE: a quotient of two bf16 values that is not a tie lies further than 2^-17 from one, so the
+// codes are those of exact arithmetic.
+//
+// A lane takes 8 values (a 16-byte load, a 4-byte store), group / 8 lanes a group.
+#include "sp24_int4.hpp"
+#include "sp24_mx4.hpp"
+
+namespace sp24 {
+namespace {
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ uint32_t f_max(uint32_t a, uint32_t b) {
+  return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+}
+// over the LANES neighbouring lanes of a group
+template <int LANES>
+__device__ __forceinline__ float group_max(float v) {
+  uint32_t b = __float_as_uint(v);
+  b = fold_lanes<2>(fold_lanes<1>(b, f_max), f_max);
+  if constexpr (LANES >= 8) b = fold_lanes<4>(b, f_max);
+  if constexpr (LANES >= 16) b = fold_lanes<8>(b, f_max);
+  return __uint_as_float(b);
+}
+
+// bf16 to nearest even; finite and not negative.  Zero becomes 1: the scale of a group of zeros.
+__device__ __forceinline__ uint32_t scale_bits(float s) {
+  const uint32_t b = f32_to_bf16_rne(s);
+  return b == 0 ? 0x3F80u : b;
+}
+
+// units of 8 values; units < 2^31 * 32
+template <int GROUP, bool ZEROS>
+__global__ __launch_bounds__(kThreads) void int4_quant_kernel(const uint16_t* __restrict__ w, int64_t units,
+                                                              uint8_t* __restrict__ codes,
+                                                              uint16_t* __restrict__ scales,
+                                                              uint8_t* __restrict__ zeros) {
+  constexpr int LANES = GROUP / 8;
+  const int64_t step = (int64_t)gridDim.x * kThreads;
+  // a group's lanes are in one wave and all of them are within the units, or none
+  for (int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x; u < units; u += step) {
+    const u32x4 d = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(w) + u);
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(d[i] << 16);
+      v[2 * i + 1] = __uint_as_float(d[i] & 0xFFFF0000u);
+    }
+    bool odd = false;  // Inf or NaN
+    float lo = 0.0f, hi = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      odd = odd || (__float_as_uint(v[i]) & 0x7F800000u) == 0x7F800000u;
+      lo = fminf(lo, v[i]);
+      hi = fmaxf(hi, v[i]);
+    }
+    if (odd) hi = __builtin_inff();  // fmaxf drops a NaN; an Inf passes through the maxima
+    hi = group_max<LANES>(hi);
+    const float neg = group_max<LANES>(-lo);  // -lo >= 0
+    odd = hi == __builtin_inff();
+    uint32_t sb;
+    float z = 8.0f;
+    if constexpr (ZEROS) {
+      const float range = hi + neg;  // beyond fp32 for the largest values: their halves are not
+      sb = scale_bits(range < __builtin_inff() ? range / 15.0f : (0.5f * hi + 0.5f * neg) / 7.5f);
+    } else {
+      sb = scale_bits(fmaxf(hi, neg) / 7.0f);
+    }
+    const float s = __uint_as_float(sb << 16);
+    if constexpr (ZEROS) z = fminf(rintf(neg / s), 15.0f);
+    uint32_t q = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float c = rintf(v[i] / s);
+      if constexpr (ZEROS) c = fminf(fmaxf(c + z, 0.0f), 15.0f);
+      else c = fminf(fmaxf(c, -8.0f), 7.0f) + 8.0f;
+      q |= (uint32_t)c << (4 * (i / 2) + 16 * (i % 2));
+    }
+    if (odd) {
+      sb = 0x7FC0u;
+      z = 8.0f;
+      q = 0x88888888u;
+    }
+    __builtin_nontemporal_store(q, reinterpret_cast<uint32_t*>(codes) + u);
+    if (u % LANES == 0) {
+      scales[u / LANES] = (uint16_t)sb;
+      if constexpr (ZEROS) zeros[u / LANES] = (uint8_t)z;
+    }
+  }
+}
+
+// (q - z) s: an integer of at most 8 bits times 8 bits is exact in fp32, and rounded once.
+__global__ __launch_bounds__(kThreads) void int4_dequant_kernel(const uint8_t* __restrict__ codes,
+                                                                const uint16_t* __restrict__ scales,
+                                                                const uint8_t* __restrict__ zeros, int64_t units,
+                                                                int lanes_log2, uint16_t* __restrict__ out) {
+  const int64_t step = (int64_t)gridDim.x * kThreads;
+  for (int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x; u < units; u += step) {
+    const uint32_t q = reinterpret_cast<const uint32_t*>(codes)[u];
+    const int64_t g = u >> lanes_log2;
+    const float s = bf16_to_f32(scales[g]), z = zeros == nullptr ? 8.0f : (float)zeros[g];
+    u32x4 o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      o[i] = f32x2_to_bf16x2(((float)(q >> (4 * i) & 15u) - z) * s, ((float)(q >> (4 * i + 16) & 15u) - z) * s);
+    __builtin_nontemporal_store(o, reinterpret_cast<u32x4*>(out) + u);
+  }
+}
+
+int blocks_for(int64_t units, int64_t most) {
+  const int64_t b = (units + kThreads - 1) / kThreads;
+  return (int)(b < most ? b : most);
+}
+constexpr int64_t kQuantBlocks = 8192, kDequantBlocks = (int64_t)1 << 22;
+
+template <int GROUP>
+hipError_t quant(const uint16_t* w, int64_t units, uint8_t* codes, uint16_t* scales, uint8_t* zeros, hipStream_t s) {
+  const dim3 grid(blocks_for(units, kQuantBlocks)), block(kThreads);
+  if (zeros != nullptr)
+    hipLaunchKernelGGL((int4_quant_kernel<GROUP, true>), grid, block, 0, s, w, units, codes, scales, zeros);
+  else
+    hipLaunchKernelGGL((int4_quant_kernel<GROUP, false>), grid, block, 0, s, w, units, codes, scales, zeros);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_quant_int4(const uint16_t* w, int64_t rows, int64_t cols, int64_t group, uint8_t* codes,
+                             uint16_t* scales, uint8_t* zeros, hipStream_t s) {
+  const int64_t units = rows * (cols / 8);
+  if (group == 32) return quant<32>(w, units, codes, scales, zeros, s);
+  if (group == 64) return quant<64>(w, units, codes, scales, zeros, s);
+  return quant<128>(w, units, codes, scales, zeros, s);
+}
+
+hipError_t launch_dequant_int4(const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros, int64_t rows,
+                               int64_t cols, int64_t group, uint16_t* out, hipStream_t s) {
+  const int64_t units = rows * (cols / 8);
+  hipLaunchKernelGGL(int4_dequant_kernel, dim3(blocks_for(units, kDequantBlocks)), dim3(kThreads), 0, s, codes, scales,
+                     zeros, units, group == 32 ? 2 : group == 64 ? 3 : 4, out);
+  return hipGetLastError();
+}
+
+}  // namespace sp24

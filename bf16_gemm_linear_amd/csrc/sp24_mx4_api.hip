@@ -17,25 +17,6 @@ bool mx4_rows(int64_t n) { return n >= 1 && n <= kMaxRows; }
 
 size_t code_bytes(int64_t rows, int64_t cols) { return (size_t)rows * (cols / 2); }
 size_t scale_bytes(int64_t rows, int64_t cols) { return (size_t)rows * (cols / 32); }
-size_t pad(size_t b) { return (b + 255) / 256 * 256; }
-
-struct Span {
-  const void* p;
-  size_t bytes;
-};
-
-// every output against every input and every other output (NULL spans are skipped)
-template <int NI, int NO>
-bool any_alias(const Span (&in)[NI], const Span (&out)[NO]) {
-  for (int o = 0; o < NO; ++o) {
-    if (out[o].p == nullptr || out[o].bytes == 0) continue;
-    for (int i = 0; i < NI; ++i)
-      if (in[i].p != nullptr && overlaps(out[o].p, out[o].bytes, in[i].p, in[i].bytes)) return true;
-    for (int j = o + 1; j < NO; ++j)
-      if (out[j].p != nullptr && overlaps(out[o].p, out[o].bytes, out[j].p, out[j].bytes)) return true;
-  }
-  return false;
-}
 
 int quant_checks(const void* wide, int64_t rows, int64_t cols, const void* codes, const void* scales, bool to_codes) {
   if (!wide || !codes || !scales) return SP24_ERR_NULL;

@@ -1,5 +1,5 @@
-// CPython binding of the MXFP4 operators and the norm: the checks of the tensors, their
-// allocation and the call in one step, since a decode step's kernels (3 to 8 us) are shorter
+// CPython binding of the MXFP4 and integer 4-bit operators, the norm, the router and the experts:
+// the checks of the tensors, their allocation and the call in one step, since a decode step's kernels (3 to 8 us) are shorter
 // than the same checks written in Python (rmsnorm 7.7 us a call through ctypes).
 //
 // The package exports these functions as they are (a Python function around each adds 0.1 to
@@ -122,6 +122,20 @@ double number(PyObject* o) {
   return v;
 }
 void* data(const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
+
+// A workspace of at least this many bytes: the given tensor if it is large enough, or a new one.
+Tensor workspace(PyObject* o, size_t bytes, const at::Device& d) {
+  Tensor ws;
+  if (!absent(o)) {
+    if (!THPVariable_Check(o)) fail(PyExc_TypeError, "ws must be a tensor");
+    ws = THPVariable_Unpack(o);
+    if (!ws.is_cuda() || ws.device() != d || !ws.is_contiguous())
+      fail(PyExc_ValueError, "ws must be contiguous and on %s", d.str().c_str());
+  }
+  if (bytes > 0 && (!ws.defined() || (size_t)ws.nbytes() < bytes))
+    ws = at::empty({(int64_t)bytes}, at::TensorOptions().dtype(at::kByte).device(d));
+  return ws;
+}
 
 PyObject* quant(PyObject* const* a) {  // x, out, scales
   const Tensor& x = need(a[0], "x", {at::kBFloat16}, 2, nullptr);
@@ -254,19 +268,139 @@ PyObject* ffn(PyObject* const* a) {
   const double eps = number(a[7]);
   const Tensor out = output(a[8], "out", {at::kBFloat16}, {n.m, n.k}, d);
   const size_t bytes = sp24_ffn_mxfp4_workspace_size(n.m, n.k, f);
-  Tensor ws;
-  if (!absent(a[10])) {
-    if (!THPVariable_Check(a[10])) fail(PyExc_TypeError, "ws must be a tensor");
-    ws = THPVariable_Unpack(a[10]);
-    if (!ws.is_cuda() || ws.device() != d || !ws.is_contiguous())
-      fail(PyExc_ValueError, "ws must be contiguous and on %s", d.str().c_str());
-  }
-  if (bytes > 0 && (!ws.defined() || (size_t)ws.nbytes() < bytes))
-    ws = at::empty({(int64_t)bytes}, at::TensorOptions().dtype(at::kByte).device(d));
+  const Tensor ws = workspace(a[10], bytes, d);
   check("sp24_ffn_mxfp4", sp24_ffn_mxfp4(n.m, n.k, f, n.x.data_ptr(), data(n.residual), data(n.residual_out),
                                          n.weight.data_ptr(), (float)eps, gu.codes, gu.scales, dn.codes, dn.scales,
                                          out.data_ptr(), data(ws), bytes, stream_of(d)));
   return pack({out, n.residual_out});
+}
+
+struct Weight4 {  // integer 4-bit: codes [rows, cols/2], scales and zeros [rows, cols/group], or with experts in front
+  const uint8_t *codes, *zeros;
+  const void* scales;
+  int64_t experts, rows, cols, group;
+};
+Weight4 weight4(PyObject* codes, PyObject* scales, PyObject* zeros, const char* name, int64_t ndim,
+                const at::Device* device) {
+  const Tensor& c = need(codes, name, {at::kByte}, ndim, device);
+  const at::Device d = c.device();
+  const Tensor& s = need(scales, "scales", {at::kBFloat16}, ndim, &d);
+  const int64_t experts = ndim == 3 ? c.size(0) : 1, rows = c.size(ndim - 2), cols = 2 * c.size(ndim - 1);
+  const int64_t groups = s.size(ndim - 1), group = groups > 0 ? cols / groups : 0;
+  if ((ndim == 3 && s.size(0) != experts) || s.size(ndim - 2) != rows || groups * group != cols ||
+      (group != 32 && group != 64 && group != 128))
+    fail(PyExc_ValueError, "%s: codes of [%lld, %lld] values need a scale of each row's groups of 32, 64 or 128", name,
+         (long long)rows, (long long)cols);
+  const uint8_t* zp = nullptr;
+  if (!absent(zeros)) {
+    const Tensor& z = need(zeros, "zeros", {at::kByte}, ndim, &d);
+    if (z.sizes() != s.sizes()) fail(PyExc_ValueError, "%s: zeros must have the shape of the scales", name);
+    zp = z.const_data_ptr<uint8_t>();
+  }
+  return Weight4{c.const_data_ptr<uint8_t>(), zp, s.const_data_ptr(), experts, rows, cols, group};
+}
+
+PyObject* quant_int4(PyObject* const* a) {  // w, group, zeros, out, scales_out, zeros_out
+  const Tensor& w = need(a[0], "w", {at::kBFloat16}, 2, nullptr);
+  const int64_t rows = w.size(0), cols = w.size(1), group = integer(a[1]);
+  if ((group != 32 && group != 64 && group != 128) || cols % group != 0)
+    fail(PyExc_ValueError, "group must be 32, 64 or 128 and divide the %lld columns, got %lld", (long long)cols,
+         (long long)group);
+  const int zeros = PyObject_IsTrue(a[2]);
+  if (zeros < 0) throw Failed{};
+  const at::Device d = w.device();
+  const Tensor out = output(a[3], "out", {at::kByte}, {rows, cols / 2}, d);
+  const Tensor scales = output(a[4], "scales_out", {at::kBFloat16}, {rows, cols / group}, d);
+  Tensor zp;
+  if (zeros) zp = output(a[5], "zeros_out", {at::kByte}, {rows, cols / group}, d);
+  else if (!absent(a[5])) fail(PyExc_ValueError, "zeros_out goes with zeros=True");
+  check("sp24_quant_int4", sp24_quant_int4(w.data_ptr(), rows, cols, group, out.data_ptr<uint8_t>(), scales.data_ptr(),
+                                           static_cast<uint8_t*>(data(zp)), stream_of(d)));
+  return pack({out, scales, zp});
+}
+
+PyObject* dequant_int4(PyObject* const* a) {  // codes, scales, zeros, out
+  const Weight4 w = weight4(a[0], a[1], a[2], "codes", 2, nullptr);
+  const at::Device d = THPVariable_Unpack(a[0]).device();
+  const Tensor out = output(a[3], "out", {at::kBFloat16}, {w.rows, w.cols}, d);
+  check("sp24_dequant_int4", sp24_dequant_int4(w.codes, w.scales, w.zeros, w.rows, w.cols, w.group, out.data_ptr(),
+                                               stream_of(d)));
+  return THPVariable_Wrap(out);
+}
+
+PyObject* gemm_int4(PyObject* const* a) {  // x, codes, scales, zeros, out
+  const Tensor& x = need(a[0], "x", {at::kBFloat16}, 2, nullptr);
+  const at::Device d = x.device();
+  const Weight4 w = weight4(a[1], a[2], a[3], "codes", 2, &d);
+  if (w.cols != x.size(1))
+    fail(PyExc_ValueError, "w has %lld columns, x has %lld", (long long)w.cols, (long long)x.size(1));
+  const Tensor out = output(a[4], "out", {at::kBFloat16}, {x.size(0), w.rows}, d);
+  check("sp24_gemm_int4", sp24_gemm_int4(x.size(0), w.rows, w.cols, w.group, x.data_ptr(), w.codes, w.scales, w.zeros,
+                                         out.data_ptr(), stream_of(d)));
+  return THPVariable_Wrap(out);
+}
+
+// logits, top, kind, bias, groups, top_groups, group_best, renormalise, factor, ids, weights
+PyObject* route(PyObject* const* a) {
+  const Tensor& l = need(a[0], "logits", {at::kFloat, at::kBFloat16}, 2, nullptr);
+  const at::Device d = l.device();
+  const int64_t tokens = l.size(0);
+  sp24_router r{};
+  r.experts = l.size(1);
+  r.logits_fp32 = l.scalar_type() == at::kFloat;
+  r.top = integer(a[1]);
+  const int64_t kind = integer(a[2]), best = integer(a[6]);
+  if (kind != SP24_ROUTE_SOFTMAX && kind != SP24_ROUTE_SIGMOID)
+    fail(PyExc_ValueError, "unknown route kind %lld", (long long)kind);
+  if (best != 1 && best != 2) fail(PyExc_ValueError, "group_best must be 1 or 2, got %lld", (long long)best);
+  r.kind = (int)kind;
+  r.groups = integer(a[4]);
+  r.top_groups = integer(a[5]);
+  r.group_best = (int)best;
+  r.renormalise = PyObject_IsTrue(a[7]);
+  if (r.renormalise < 0) throw Failed{};
+  r.factor = (float)number(a[8]);
+  const float* bias = nullptr;
+  if (!absent(a[3])) {
+    const Tensor& b = need(a[3], "bias", {at::kFloat}, 1, &d);
+    if (b.numel() != r.experts) fail(PyExc_ValueError, "bias must hold %lld values", (long long)r.experts);
+    bias = b.const_data_ptr<float>();
+  }
+  if (r.groups < 1 || r.experts % r.groups != 0 || r.top_groups < 1 || r.top_groups > r.groups || r.top < 1 ||
+      r.top > r.top_groups * (r.experts / r.groups))
+    fail(PyExc_ValueError, "%lld experts cannot be chosen from %lld of %lld groups of %lld experts", (long long)r.top,
+         (long long)r.top_groups, (long long)r.groups, (long long)r.experts);
+  const Tensor ids = output(a[9], "ids", {at::kInt}, {tokens, r.top}, d);
+  const Tensor weights = output(a[10], "weights", {at::kFloat}, {tokens, r.top}, d);
+  check("sp24_route", sp24_route(&r, tokens, l.const_data_ptr(), bias, ids.data_ptr<int32_t>(),
+                                 weights.data_ptr<float>(), stream_of(d)));
+  return pack({ids, weights});
+}
+
+// x, ids, weights, gu_codes, gu_scales, down_codes, down_scales, gu_zeros, down_zeros, out, ws
+PyObject* experts_int4(PyObject* const* a) {
+  const Tensor& x = need(a[0], "x", {at::kBFloat16}, 2, nullptr);
+  const at::Device d = x.device();
+  const Tensor& ids = need(a[1], "ids", {at::kInt}, 2, &d);
+  const Tensor& weights = need(a[2], "weights", {at::kFloat}, 2, &d);
+  const Weight4 gu = weight4(a[3], a[4], a[7], "gu_codes", 3, &d), dn = weight4(a[5], a[6], a[8], "down_codes", 3, &d);
+  const int64_t tokens = x.size(0), top = ids.size(1), f = dn.cols;
+  if (ids.size(0) != tokens || weights.sizes() != ids.sizes())
+    fail(PyExc_ValueError, "ids and weights must be [%lld, top]", (long long)tokens);
+  if (gu.cols != x.size(1) || dn.rows != gu.cols || gu.rows != 2 * f || dn.experts != gu.experts ||
+      dn.group != gu.group)
+    fail(PyExc_ValueError, "experts of [%lld, %lld] and [%lld, %lld] values (groups of %lld and %lld) do not fit "
+         "tokens of %lld", (long long)gu.rows, (long long)gu.cols, (long long)dn.rows, (long long)dn.cols,
+         (long long)gu.group, (long long)dn.group, (long long)x.size(1));
+  const Tensor out = output(a[9], "out", {at::kBFloat16}, {tokens, gu.cols}, d);
+  const size_t bytes = sp24_experts_int4_workspace_size(tokens, gu.cols, f, gu.experts, top);
+  const Tensor ws = workspace(a[10], bytes, d);
+  const sp24_int4_experts w{gu.experts, gu.cols, f, gu.group, gu.codes, gu.scales, gu.zeros, dn.codes, dn.scales,
+                            dn.zeros};
+  check("sp24_experts_int4", sp24_experts_int4(&w, tokens, top, x.data_ptr(), ids.const_data_ptr<int32_t>(),
+                                               weights.const_data_ptr<float>(), out.data_ptr(), data(ws), bytes,
+                                               stream_of(d)));
+  return THPVariable_Wrap(out);
 }
 
 // A function's parameters by name, with the values of those that may be left out.
@@ -290,6 +424,15 @@ Function g_rmsnorm{"rmsnorm", rmsnorm, 2, 9,
 Function g_ffn{"ffn_mxfp4", ffn, 6, 11,
                {"x", "weight", "gu_codes", "gu_scales", "down_codes", "down_scales", "residual", "eps", "out",
                 "residual_out", "ws"}};
+Function g_quant4{"quant_int4", quant_int4, 1, 6, {"w", "group", "zeros", "out", "scales_out", "zeros_out"}};
+Function g_dequant4{"dequant_int4", dequant_int4, 2, 4, {"codes", "scales", "zeros", "out"}};
+Function g_gemm4{"gemm_int4", gemm_int4, 3, 5, {"x", "codes", "scales", "zeros", "out"}};
+Function g_route{"route", route, 2, 11,
+                 {"logits", "top", "kind", "bias", "groups", "top_groups", "group_best", "renormalise", "factor",
+                  "ids", "weights"}};
+Function g_experts{"experts_int4", experts_int4, 7, 11,
+                   {"x", "ids", "weights", "gu_codes", "gu_scales", "down_codes", "down_scales", "gu_zeros",
+                    "down_zeros", "out", "ws"}};
 
 // Arguments by position and by name into the function's order.
 void place(const Function& f, PyObject* const* args, Py_ssize_t count, PyObject* names, PyObject** to) {
@@ -406,6 +549,38 @@ A pre-norm feed-forward block in MXFP4: y = down(silu(gate(v)) * up(v)), v the R
 x (+ residual) under `weight`; gate_up W [2 f, d] (gate rows first) and down W [d, f] as MXFP4
 codes and scales.  Returns (y bf16 [m, d], residual_out or None); bit for bit rmsnorm(NORM_MXFP4),
 gated_mxfp4(quantise=True) and gemm_mxfp4 in turn.)"),
+    method<g_quant4>(R"(quant_int4(w, group=128, zeros=False, out=None, scales_out=None, zeros_out=None)
+--
+
+bf16 [rows, cols] (cols % group == 0, group 32, 64 or 128) -> integer 4-bit (codes uint8 [rows,
+cols/2], scales bf16 [rows, cols/group], zeros uint8 [rows, cols/group] or None): values (q - z) s,
+symmetric around 8 or, with zeros=True, between a group's least and largest.  pack_int4 puts codes
+from elsewhere into this order.)"),
+    method<g_dequant4>(R"(dequant_int4(codes, scales, zeros=None, out=None)
+--
+
+The bf16 values [rows, cols] that integer 4-bit codes, scales and zero points stand for.)"),
+    method<g_gemm4>(R"(gemm_int4(x, codes, scales, zeros=None, out=None)
+--
+
+Y = X . W^T, X bf16 [m, k], W [n, k] in integer 4-bit with group scales; bf16 [m, n].)"),
+    method<g_route>(R"(route(logits, top, kind=0, bias=None, groups=1, top_groups=1, group_best=1, renormalise=True, factor=1.0, ids=None, weights=None)
+--
+
+The experts of each token and their weights: (ids int32 [tokens, top], weights fp32 [tokens, top]),
+the best first, from logits bf16 or fp32 [tokens, experts].
+
+Scores are the softmax (ROUTE_SOFTMAX, the default kind) or the sigmoid (ROUTE_SIGMOID) of the
+logits; `bias` (fp32 [experts]) is added for the choice alone.  groups > 1: only experts of the
+top_groups groups whose group_best best experts sum to most.  renormalise: the chosen scores are
+divided by their sum.  Weights are times factor.  Ties go to the lower index; -inf masks an expert.)"),
+    method<g_experts>(R"(experts_int4(x, ids, weights, gu_codes, gu_scales, down_codes, down_scales, gu_zeros=None, down_zeros=None, out=None, ws=None)
+--
+
+The feed-forward block of experts over integer 4-bit weights: y[t] = sum over j of weights[t, j] *
+down_e(silu(gate_e(x[t])) * up_e(x[t])), e = ids[t, j]; bf16 [tokens, d].  gate_up W [experts, 2 f, d]
+(gate rows first) and down W [experts, d, f] as codes and scales (and zeros) of quant_int4 with the
+experts stacked.  An id outside the experts adds nothing.)"),
     {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
@@ -418,14 +593,23 @@ bool intern(Function& f) {
   return true;
 }
 bool prepare() {
-  for (Function* f : {&g_quant, &g_dequant, &g_gemm, &g_gated, &g_rmsnorm, &g_ffn})
+  for (Function* f : {&g_quant, &g_dequant, &g_gemm, &g_gated, &g_rmsnorm, &g_ffn, &g_quant4, &g_dequant4, &g_gemm4, &g_route, &g_experts})
     if (!intern(*f)) return false;
   PyObject* const eps = PyFloat_FromDouble(1e-6);
   g_gated.defaults[4] = Py_False;
   g_rmsnorm.defaults[2] = PyLong_FromLong(SP24_NORM_BF16);
   g_rmsnorm.defaults[5] = PyLong_FromLong(128);
   g_rmsnorm.defaults[4] = g_ffn.defaults[7] = eps;
-  return eps != nullptr && g_rmsnorm.defaults[2] != nullptr && g_rmsnorm.defaults[5] != nullptr;
+  g_quant4.defaults[1] = PyLong_FromLong(128);
+  g_quant4.defaults[2] = Py_False;
+  PyObject* const one = PyLong_FromLong(1);
+  g_route.defaults[2] = PyLong_FromLong(SP24_ROUTE_SOFTMAX);
+  g_route.defaults[4] = g_route.defaults[5] = g_route.defaults[6] = one;
+  g_route.defaults[7] = Py_True;
+  g_route.defaults[8] = PyFloat_FromDouble(1.0);
+  return eps != nullptr && g_rmsnorm.defaults[2] != nullptr && g_rmsnorm.defaults[5] != nullptr &&
+         g_quant4.defaults[1] != nullptr && one != nullptr && g_route.defaults[2] != nullptr &&
+         g_route.defaults[8] != nullptr;
 }
 
 }  // namespace

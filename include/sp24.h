@@ -558,6 +558,104 @@ int sp24_ffn_mxfp4(int64_t m, int64_t d, int64_t f, const void* x_bf16, const vo
  * then rejects).  Host-only. */
 size_t sp24_ffn_mxfp4_workspace_size(int64_t m, int64_t d, int64_t f);
 
+/* ---------------------------------------------------------------------------
+ * Integer 4-bit weights with a scale per group, beside bf16 activations, and a
+ * feed-forward block of experts over them.  A group is `group` (32, 64 or 128)
+ * consecutive values of a row; a value is (q - z) * s.
+ *   codes  [rows, cols/2] bytes: q in 0..15.  Eight values of a row share a
+ *          little-endian 32-bit word, value j at bits 4*(j/2) + 16*(j%2);
+ *   scales [rows, cols/group] bf16: s;
+ *   zeros  [rows, cols/group] bytes: z, or NULL: 8 everywhere.
+ * cols % group == 0 everywhere.
+ * ------------------------------------------------------------------------- */
+
+/* bf16 [rows, cols] -> codes and scales, and with zeros_out zero points.
+ *   zeros_out NULL: s = bf16_rne(amax / 7), q = clamp(rne(w / s), -8, 7) + 8;
+ *   else lo = min(0, min w), hi = max(0, max w), s = bf16_rne((hi - lo) / 15),
+ *     z = clamp(rne(-lo / s), 0, 15), q = clamp(rne(w / s) + z, 0, 15);
+ * s = 1 where that is 0.  fp32 arithmetic, IEEE divisions.  A group with an Inf or a
+ * NaN gets s = NaN and q = z = 8.
+ *   1 <= rows <= 2^21, group <= cols <= 2^20.  No workspace. */
+int sp24_quant_int4(const void* w_bf16, int64_t rows, int64_t cols, int64_t group, uint8_t* codes_out,
+                    void* scales_out_bf16, uint8_t* zeros_out, void* stream);
+
+/* The values (q - z) * s, rounded once to bf16.  Limits as sp24_quant_int4. */
+int sp24_dequant_int4(const uint8_t* codes, const void* scales_bf16, const uint8_t* zeros, int64_t rows, int64_t cols,
+                      int64_t group, void* out_bf16, void* stream);
+
+/* Y = X . W^T, X bf16 [m, k], W [n, k] as above, Y bf16 [m, n].  Sums over a group in
+ * fp32 of x * (q - z), which is exact in each product; times s and summed over the
+ * groups in fp32; rounded once.  The order of the sums is fixed for a given (m, n, k):
+ * results are bitwise reproducible.  A token with an Inf or a NaN has Inf or NaN in
+ * its row of Y, and only there; finite values of X reach up to 2^119.
+ * Requires m, n >= 1, at most 2^21; group <= k <= 2^20.  No workspace.
+ * (SP24_ERR_HIP where no grid covers the outputs: beyond 2^32 of them.) */
+int sp24_gemm_int4(int64_t m, int64_t n, int64_t k, int64_t group, const void* x_bf16, const uint8_t* codes,
+                   const void* scales_bf16, const uint8_t* zeros, void* y_bf16, void* stream);
+
+typedef enum sp24_route_kind { SP24_ROUTE_SOFTMAX = 0, SP24_ROUTE_SIGMOID = 1 } sp24_route_kind;
+
+/* A router: which experts a row of logits l stands for, and with which weights.
+ *   score_i  = softmax(l)_i or sigmoid(l_i);
+ *   choice_i = score_i + bias_i, without a bias l_i itself; -inf where l_i is -inf (a
+ *              masked expert) or a NaN;
+ *   groups > 1: the experts are that many groups of experts / groups neighbours; a
+ *              group's value is the sum of its group_best (1 or 2) largest choices
+ *              (without a bias and with group_best 2, scores), masked ones left out,
+ *              and only experts of the top_groups best groups are chosen from;
+ *   ids      = the `top` experts of the largest choice, largest first;
+ *   weights  = score * factor, or with renormalise score / (sum of the chosen scores)
+ *              * factor; 0 where that sum is 0.
+ * Equal values: the lower index first, for experts and groups.  Ids are always
+ * different experts; masked ones come last, with weight 0.  +inf counts as the largest
+ * number.  Scores that a choice depends on are formed and compared in fp64. */
+typedef struct sp24_router {
+  int kind;            /* sp24_route_kind */
+  int logits_fp32;     /* 1: logits are fp32, 0: bf16 */
+  int64_t experts;     /* 1..1024 */
+  int64_t top;         /* 1..64, at most the experts of top_groups groups */
+  int64_t groups;      /* 1..64, divides experts */
+  int64_t top_groups;  /* 1..groups */
+  int group_best;      /* 1, or 2 with at least 2 experts in a group */
+  int renormalise;
+  float factor;        /* finite */
+} sp24_router;
+
+/* logits [tokens, experts] -> ids int32 [tokens, top], weights fp32 [tokens, top].
+ *   bias_f32 [experts] or NULL.  1 <= tokens <= 2^21.  No workspace. */
+int sp24_route(const sp24_router* router, int64_t tokens, const void* logits, const float* bias_f32, int32_t* ids_out,
+               float* weights_out, void* stream);
+
+/* The weights of a block of experts: per expert a gate-over-up weight [2f, d] (the f
+ * gate rows first) and a down weight [d, f], the experts' one after the other. */
+typedef struct sp24_int4_experts {
+  int64_t experts, d, f, group;
+  const uint8_t* gu_codes;      /* [experts, 2f, d/2] */
+  const void* gu_scales_bf16;   /* [experts, 2f, d/group] */
+  const uint8_t* gu_zeros;      /* the same shape, or NULL */
+  const uint8_t* down_codes;    /* [experts, d, f/2] */
+  const void* down_scales_bf16; /* [experts, d, f/group] */
+  const uint8_t* down_zeros;    /* the same shape, or NULL */
+} sp24_int4_experts;
+
+/* The feed-forward block of experts:
+ *   h = bf16_rne(silu(x Wg_e^T) * (x Wu_e^T)),  e = ids[t, j],
+ *   y[t] = bf16_rne(sum over j of weights[t, j] * (h Wd_e^T)),
+ * products as sp24_gemm_int4, the sum over j in fp32 in the order of j.  A pair whose id
+ * is outside 0..experts-1 adds nothing (a padded token; experts that live elsewhere); an
+ * id that comes twice for a token adds twice.
+ *   x_bf16 [tokens, d]; ids [tokens, top]; weights_f32 [tokens, top]; y_bf16 [tokens, d].
+ * Requires 1 <= experts <= 1024, 1 <= top <= 64, tokens >= 1, tokens * top <= 2^21,
+ * group <= d, f <= 2^20, d % group == f % group == 0.
+ *   ws/ws_bytes: sp24_experts_int4_workspace_size(tokens, d, f, experts, top).  No host
+ * synchronisation. */
+int sp24_experts_int4(const sp24_int4_experts* w, int64_t tokens, int64_t top, const void* x_bf16, const int32_t* ids,
+                      const float* weights_f32, void* y_bf16, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of sp24_experts_int4 (0 for invalid sizes, which the call itself then
+ * rejects).  Host-only. */
+size_t sp24_experts_int4_workspace_size(int64_t tokens, int64_t d, int64_t f, int64_t experts, int64_t top);
+
 /* Workspace bytes needed by an op at a shape (0 if none; also 0 for invalid
  * arguments, which the op itself then rejects). */
 size_t sp24_workspace_size(int op, int dtype, int64_t m, int64_t n, int64_t k);
