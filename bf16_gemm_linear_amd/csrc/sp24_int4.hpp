@@ -80,6 +80,20 @@ struct Int4Experts {
 };
 hipError_t launch_int4_experts(const Int4Experts& a, hipStream_t s);
 
+// The kernels.  sp24_int4_vec.hip: a few tokens; the experts' block with pairs in their own order, y being
+// its output.
+hipError_t launch_int4_vec(const Int4Gemm& g, hipStream_t s);
+hipError_t launch_int4_vec_experts(const Int4Experts& e, const int32_t* ids, const float* weights, uint16_t* y,
+                                   hipStream_t s);
+// sp24_int4_stream.hip: rb row blocks of 16, 16 mb tokens and `cols` output columns a workgroup.
+hipError_t launch_int4_stream(int rb, int mb, int cols, const Int4Gemm& g, hipStream_t s);
+hipError_t launch_int4_stream_gated(int rb, int mb, int cols, const Int4Experts& e, hipStream_t s);
+hipError_t launch_int4_stream_down(int rb, int mb, int cols, const Int4Experts& e, hipStream_t s);
+// sp24_int4_tiled.hip: configuration cfg.
+hipError_t launch_int4_tiled(int cfg, const Int4Gemm& g, hipStream_t s);
+hipError_t launch_int4_tiled_gated(int cfg, const Int4Experts& e, hipStream_t s);
+hipError_t launch_int4_tiled_down(int cfg, const Int4Experts& e, hipStream_t s);
+
 // sp24_experts.hip: pairs whose id is outside 0 .. experts - 1 get no place and add nothing.
 hipError_t launch_sort_pairs(const int32_t* ids, int64_t count, int experts, int* offsets, int* order, hipStream_t s);
 hipError_t launch_join_pairs(const float* part, const int32_t* ids, const float* weights, int64_t tokens, int top,

@@ -1,0 +1,314 @@
+// Products with integer 4-bit weights for many tokens, over LDS tiles: the matrix instructions are the
+// time.
+//
+// A workgroup owns BM rows of X by BN rows of W (GATED: per wave 32 gate rows and their up rows) and
+// walks K in steps of 64 values with two buffers in LDS: X straight from global memory (global_load_lds), W
+// through registers, where a thread widens 32 codes of a row to bf16 for the next step while
+// this one is multiplied: every code is widened once for BM rows of X.
+//
+// No value of W is rounded: with a group's scale as m 2^e, 1 <= m < 2, what is multiplied is (q - z) 2^e, which
+// bf16 holds exactly, and the sums are kept in units of the group's m: where a group ends they are multiplied by
+// m / m', between 1/2 and 2, one instruction a sum and group, and by the last m at the end.  (A second
+// set of accumulators for a group's sums does not fit beside the 256 x 256 tile's first; rounding
+// (q - z) s to bf16 instead takes less time, but its errors, 2^-9 of each, were up to 3 half steps of bf16
+// where a few channels of X are 20 times as large as the others.)
+//
+// v_mfma_f32_32x32x16_bf16, A = X, B = W: lane l holds row l % 32 and values 8 (l / 32) .. + 7;
+// accumulator register 4 g + e is token 8 g + 4 (l / 32) + e, W row l % 32.  LDS rows of 128 bytes are
+// XOR-swizzled in pieces of 16; the swizzle of X is applied on the global side.
+#include "sp24_dma.hpp"
+#include "sp24_int4.hpp"
+#include "sp24_mx4.hpp"
+
+namespace sp24 {
+namespace {
+
+enum { PLAIN = 0, GATED = 1, DOWN = 2 };
+constexpr int KS = 64, RB = KS * 2, P = RB / 16;  // a step: values, bytes and 16-byte pieces of a row
+
+struct Args {
+  int m, n, k, group;
+  const uint16_t* x;
+  Int4Weight w;
+  uint16_t* y;
+  float* part;
+  Pairs pairs;
+  int tiles, nblocks;  // row tiles (at most) and column tiles
+};
+
+// XS buffers of X in LDS (XS - 1 steps ahead), WS sets of W's codes in registers (WS steps ahead).
+template <int BM_, int BN_, int WM_, int WN_, int XS_, int WS_, int OCC_>
+struct TileCfg {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, XS = XS_, WS = WS_, OCC = OCC_;
+  static constexpr int NT = WM * WN * 64, TI = BM / WM / 32, TJ = BN / WN / 32;
+  static constexpr int X_I = BM / 8 / (WM * WN);  // load instructions of X a wave and step
+  static constexpr int X_BYTES = BM * RB, W_BYTES = BN * RB, M_OFF = XS * X_BYTES + 2 * W_BYTES;
+  static constexpr int LDS = M_OFF + 2 * 2 * BN * 4;  // and m of every row's two blocks of 32, two buffers
+  static_assert(X_I * 8 * WM * WN == BM && NT == BN * 2 && TI > 0 && TJ > 0 && LDS <= 160 * 1024, "tile");
+  // loads of a wave that can be outstanding while the X of a step has to be there: X of the steps behind it, and
+  // W's codes and scales (and zero points: then fewer are) issued since
+  static constexpr int LATER = (XS - 2) * X_I + (XS - 1) * 2;
+};
+
+// 8 codes -> 8 bf16 values (q - z) s; ns = -z s, s a power of two.
+__device__ __forceinline__ u32x4 widen(uint32_t w, float s, float ns) {
+  uint32_t e = w & 0x0F0F0F0Fu, o = (w >> 4) & 0x0F0F0F0Fu;
+  asm("" : "+v"(e), "+v"(o));  // or the compiler takes the codes out of w one by one: an instruction more for most
+  // bytes of e: values 0 4 1 5, of o: 2 6 3 7
+  auto f = [&](uint32_t b, int i) { return fmaf((float)((b >> (8 * i)) & 255u), s, ns); };
+  return u32x4{f32x2_to_bf16x2(f(e, 0), f(e, 2)), f32x2_to_bf16x2(f(o, 0), f(o, 2)),
+               f32x2_to_bf16x2(f(e, 1), f(e, 3)), f32x2_to_bf16x2(f(o, 1), f(o, 3))};
+}
+
+template <class C, int MODE>
+__global__ __launch_bounds__(C::NT, C::OCC) void int4_tiled_kernel(Args p) {
+  constexpr int TI = C::TI, TJ = C::TJ, H = MODE == GATED ? 2 : 1;
+  static_assert(MODE != GATED || TJ == 2, "a wave's gate tile and its up tile");
+  __shared__ __attribute__((aligned(16))) uint8_t lds[C::LDS];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / C::WN, wn = wave % C::WN;
+
+  // Workgroups go to the 8 XCDs in turn; each XCD takes a run of tiles, all row tiles of a column
+  // tile next to each other, so that its L2 holds the W and X that they share.
+  const int total = p.tiles * p.nblocks, run = (total + 7) / 8;
+  const int number = (int)(blockIdx.x % 8) * run + (int)(blockIdx.x / 8);
+  if ((int)(blockIdx.x / 8) >= run || number >= total) return;
+  int expert = 0, first, rows, nb;
+  if constexpr (MODE == PLAIN) {
+    first = number % p.tiles * C::BM;
+    nb = number / p.tiles;
+    rows = min(C::BM, p.m - first);
+  } else {
+    nb = number % p.nblocks;
+    if (!find_tile<C::BM>(p.pairs, number / p.nblocks, lane, expert, first, rows)) return;
+  }
+  const int n0 = nb * (C::BN / H);
+
+  // X: this lane's rows (of 8 an instruction), swizzled piece
+  const uint16_t* xrow[C::X_I];
+#pragma unroll
+  for (int j = 0; j < C::X_I; ++j) {
+    const int r = (wave * C::X_I + j) * 8 + lane / P;
+    size_t row = first + min(r, rows - 1);
+    if constexpr (MODE == GATED) row = p.pairs.order[row] / p.pairs.top;
+    xrow[j] = p.x + row * p.k;
+  }
+  // W: this thread has half `wh` (32 values of a step) of LDS row wr
+  const int groups = p.k / p.group, gshift = p.group == 32 ? 5 : p.group == 64 ? 6 : 7;
+  const int wh = tid & 1, wr = tid / 2;
+  size_t wrow;
+  {
+    int col = n0 + wr, half = 0;
+    if constexpr (MODE == GATED) {  // a wave's 64 rows: 32 gate rows, their up rows
+      col = n0 + wr / 64 * 32 + wr % 32;
+      half = wr / 32 % 2;
+    }
+    wrow = (size_t)expert * (H * p.n) + (size_t)half * p.n + min(col, p.n - 1);
+  }
+  const uint8_t* const wcode = p.w.codes + wrow * (p.k / 2);
+  const uint16_t* const wscale = p.w.scales + wrow * groups;
+  const uint8_t* const wzero = p.w.zeros == nullptr ? nullptr : p.w.zeros + wrow * groups;
+
+  const int steps = (p.k + KS - 1) / KS;
+  // Loads past the last step are that step's again, so that every step has the same number of them.
+  auto issue_x = [&](int t, int buffer) {
+    const int k0 = min(t, steps - 1) * KS;
+    uint8_t* buf = lds + buffer * C::X_BYTES;
+#pragma unroll
+    for (int j = 0; j < C::X_I; ++j) {
+      const int i = wave * C::X_I + j, r = i * 8 + lane / P;
+      // past k: the row's last piece again, against values of W that are 0
+      const int at = min(k0 + 8 * swz16<P>(r, lane % P), p.k - 8);
+      dma16(xrow[j] + at, buf + i * 1024);
+    }
+  };
+  struct Codes {
+    u32x4 q;
+    uint32_t s, z;
+  };
+  auto load_w = [&](Codes& c, int t) {
+    const int k = min(t * KS + 32 * wh, p.k - 32);
+    c.q = *reinterpret_cast<const u32x4*>(wcode + k / 2);
+    c.s = wscale[k >> gshift];
+    c.z = p.w.zeros == nullptr ? kInt4Zero : wzero[k >> gshift];
+  };
+  uint8_t* const wlds = lds + C::XS * C::X_BYTES;
+  float* const mlds = reinterpret_cast<float*>(lds + C::M_OFF);
+  // values 8 d .. 8 d + 7 of the thread's 32 of step t
+  auto store_w = [&](const Codes& c, int t, int d) {
+    // 2^e: the exponent's bits alone (2^-126 for subnormals, whose m is below 1; Inf and NaN: Inf).  Past k and
+    // with a scale of 0: values 0 whatever the codes, and m = 1.
+    const bool none = t * KS + 32 * wh >= p.k || (c.s & 0x7FFFu) == 0;
+    const uint32_t exponent = (c.s & 0x7F80u) << 16;
+    const float s = none ? 0.0f : __uint_as_float(max(exponent, 0x00800000u));
+    *reinterpret_cast<u32x4*>(wlds + (t & 1) * C::W_BYTES + wr * RB + 16 * swz16<P>(wr, 4 * wh + d)) =
+        widen(c.q[d], s, -(float)c.z * s);
+    if (d == 0) {
+      // the mantissa and the sign, in 1's binade; a subnormal's without the leading bit; NaN stays one
+      const uint32_t one = (c.s & 0x807Fu) << 16 | 0x3F800000u;
+      float m = __uint_as_float(one);
+      if (exponent == 0) m -= __uint_as_float((c.s & 0x8000u) << 16 | 0x3F800000u);
+      if (exponent == 0x7F800000u) m = (c.s & 0x7Fu) != 0 ? __builtin_nanf("") : __uint_as_float(one & 0xFF800000u);
+      mlds[((t & 1) * 2 + wh) * C::BN + wr] = none ? 1.0f : m;
+    }
+  };
+
+  f32x16 acc[TI][TJ];
+#pragma unroll
+  for (int i = 0; i < TI; ++i)
+#pragma unroll
+    for (int j = 0; j < TJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+
+  auto fence = [] {  // the loads of W stay where they are among those of X: the waits count on it
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  Codes c[C::WS];
+  issue_x(0, 0);
+  fence();
+  load_w(c[0], 0);
+#pragma unroll
+  for (int u = 1; u < C::XS - 1; ++u) issue_x(u, u);
+  fence();
+#pragma unroll
+  for (int d = 0; d < 4; ++d) store_w(c[0], 0, d);
+#pragma unroll
+  for (int u = 1; u <= C::WS; ++u) {
+    load_w(c[u % C::WS], u);
+    fence();
+  }
+  // The waves take the 32-row parts of the tile in turn: a tile with few rows is shared, and parts without any are
+  // not multiplied.
+  const int live = MODE == PLAIN ? TI : ((rows + 31) / 32 - wm + C::WM - 1) / C::WM;
+  float unit[TJ];  // the sums are times this
+#pragma unroll
+  for (int j = 0; j < TJ; ++j) unit[j] = 1.0f;
+  int xbuf = 0, xnext = C::XS - 1;
+  for (int t0 = 0; t0 < steps; t0 += C::WS) {
+#pragma unroll
+    for (int u = 0; u < C::WS; ++u) {
+      const int t = t0 + u;
+      if (t >= steps) break;
+      // X of this step has arrived, everybody's part of W is written, and the other buffers are read
+      __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+      if (t < C::XS) wait_vmcnt<0>();      // the first loads were issued in another order
+      else wait_vmcnt<C::LATER>();
+      __builtin_amdgcn_s_barrier();
+      fence();
+      issue_x(t + C::XS - 1, xnext);
+      fence();
+      const uint8_t* xb = lds + xbuf * C::X_BYTES;
+      const uint8_t* wb = wlds + (t & 1) * C::W_BYTES;
+      bf16x8 a[2][TI], b[2][TJ];
+      auto read = [&](int kk) {
+#pragma unroll
+        for (int i = 0; i < TI; ++i) {
+          if (i > 0 && i >= live) continue;  // uniform: no rows there
+          const int r = (i * C::WM + wm) * 32 + (lane & 31);
+          a[kk & 1][i] = __builtin_bit_cast(
+              bf16x8, *reinterpret_cast<const u32x4*>(xb + r * RB + 16 * swz16<P>(r, 2 * kk + (lane >> 5))));
+        }
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) {
+          const int r = (wn * TJ + j) * 32 + (lane & 31);
+          b[kk & 1][j] = __builtin_bit_cast(
+              bf16x8, *reinterpret_cast<const u32x4*>(wb + r * RB + 16 * swz16<P>(r, 2 * kk + (lane >> 5))));
+        }
+      };
+      // at the first step of a group (groups of 32: twice a step)
+      auto rescale = [&](int h) {
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) {
+          const float m = mlds[((t & 1) * 2 + h) * C::BN + (wn * TJ + j) * 32 + (lane & 31)];
+          const float f = unit[j] / m;
+          unit[j] = m;
+#pragma unroll
+          for (int i = 0; i < TI; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[i][j][e] *= f;
+        }
+      };
+      read(0);
+      if (p.group != 128 || (t & 1) == 0) rescale(0);
+#pragma unroll
+      for (int kk = 0; kk < KS / 16; ++kk) {
+        if (kk == 2 && p.group == 32) rescale(1);
+        if (kk + 1 < KS / 16) read(kk + 1);  // while this one is multiplied
+#pragma unroll
+        for (int i = 0; i < TI; ++i)
+#pragma unroll
+          for (int j = 0; j < TJ; ++j)
+            if (i == 0 || i < live)
+              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[kk & 1][i], b[kk & 1][j], acc[i][j], 0, 0, 0);
+        store_w(c[(u + 1) % C::WS], t + 1, kk);  // past the last step: into a buffer that nobody reads
+      }
+      load_w(c[(u + 1) % C::WS], t + 1 + C::WS);
+      fence();
+      xbuf = xbuf + 1 == C::XS ? 0 : xbuf + 1;
+      xnext = xnext + 1 == C::XS ? 0 : xnext + 1;
+    }
+  }
+  wait_vmcnt<0>();  // loads into LDS end before the workgroup does
+
+#pragma unroll
+  for (int i = 0; i < TI; ++i)
+#pragma unroll
+    for (int j = 0; j < TJ / H; ++j) {
+      const int col = n0 + (wn * (TJ / H) + j) * 32 + (lane & 31);
+      if (col >= p.n) continue;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int row = (i * C::WM + wm) * 32 + 8 * (e / 4) + 4 * (lane >> 5) + e % 4;
+        if (row >= rows) continue;
+        float v = acc[i][j][e] * unit[j];
+        if constexpr (MODE == GATED) v = silu_mul(v, acc[i][TJ - 1][e] * unit[TJ - 1]);
+        if constexpr (MODE == DOWN) p.part[(size_t)p.pairs.order[first + row] * p.n + col] = v;
+        else p.y[(size_t)(first + row) * p.n + col] = (uint16_t)f32x2_to_bf16x2(v, 0.0f);
+      }
+    }
+}
+
+template <class C, int MODE>
+hipError_t launch(Args a, int64_t tiles, hipStream_t s) {
+  constexpr int cols = MODE == GATED ? C::BN / 2 : C::BN;
+  a.nblocks = (a.n + cols - 1) / cols;
+  if (tiles * a.nblocks >= (int64_t)1 << 31) return hipErrorInvalidConfiguration;
+  a.tiles = (int)tiles;
+  const int64_t grid = (tiles * a.nblocks + 7) / 8 * 8;
+  if (grid * C::NT >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;  // HIP counts threads in 32 bits
+  hipLaunchKernelGGL((int4_tiled_kernel<C, MODE>), dim3((uint32_t)grid), dim3(C::NT), 0, s, a);
+  return hipGetLastError();
+}
+
+template <int MODE, class F>
+hipError_t by_size(int cfg, Args a, F tiles, hipStream_t s) {
+  switch (cfg) {
+    case 0: return launch<TileCfg<256, 256, 2, 4, 2, 2, 2>, MODE>(a, tiles(256), s);
+    case 1: return launch<TileCfg<128, 256, 2, 4, 4, 3, 2>, MODE>(a, tiles(128), s);
+    case 2: return launch<TileCfg<128, 128, 2, 2, 2, 2, 2>, MODE>(a, tiles(128), s);
+    case 3: return launch<TileCfg<64, 128, 2, 2, 4, 3, 2>, MODE>(a, tiles(64), s);
+  }
+  return hipErrorInvalidConfiguration;
+}
+
+}  // namespace
+
+hipError_t launch_int4_tiled(int cfg, const Int4Gemm& g, hipStream_t s) {
+  const Args a{g.m, g.n, g.k, g.group, g.x, g.w, g.y, nullptr, Pairs{}, 0, 0};
+  return by_size<PLAIN>(cfg, a, [&](int bm) { return ((int64_t)g.m + bm - 1) / bm; }, s);
+}
+
+hipError_t launch_int4_tiled_gated(int cfg, const Int4Experts& e, hipStream_t s) {
+  const Args a{0, e.f, e.d, e.group, e.x, e.gu, e.h, nullptr, e.pairs, 0, 0};
+  return by_size<GATED>(cfg, a, [&](int bm) { return most_tiles(e.pairs.count, e.pairs.experts, bm); }, s);
+}
+
+hipError_t launch_int4_tiled_down(int cfg, const Int4Experts& e, hipStream_t s) {
+  const Args a{0, e.d, e.f, e.group, e.h, e.down, nullptr, e.part, e.pairs, 0, 0};
+  return by_size<DOWN>(cfg, a, [&](int bm) { return most_tiles(e.pairs.count, e.pairs.experts, bm); }, s);
+}
+
+}  // namespace sp24

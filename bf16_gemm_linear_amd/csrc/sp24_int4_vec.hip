@@ -1,0 +1,208 @@
+// Products with integer 4-bit weights for one to four tokens: the weight's bytes are the time.
+//
+// A workgroup holds RB rows of W, a wave of it a chunk of 2048 values of K, lane l of it the 32 values of block l: each
+// row's load is 1 KB of neighbouring bytes, and the lane's x stays in registers for all rows.  No LDS
+// before the end, no waits between waves: what is in flight at once is a decode step's whole share of
+// W (n = 14336, k = 4096: 14 waves a CU of 8 KB each).
+// Two values at a time: (128 + q) as bf16 pairs (shift, and-or), then v_dot2_f32_bf16, 11
+// instructions for 8 values and one token.  A group's scale and zero come in behind the block's sum:
+// s (sum x (128 + q) - (128 + z) sum x), in fp32; a block of 32 lies in one group.
+// The lanes' sums are joined by register exchanges (rows and lanes transposed on the way), those of
+// the chunks through LDS, in a fixed order.
+#include "sp24_int4.hpp"
+#include "sp24_mx4.hpp"
+
+namespace sp24 {
+namespace {
+
+enum { PLAIN = 0, GATED = 1, DOWN = 2 };
+
+struct Args {
+  int m, n, k, group;  // n: output columns (GATED: W has 2 n rows an expert)
+  const uint16_t* x;
+  Int4Weight w;
+  uint16_t* y;
+  // GATED, DOWN: pairs in their own order (pair t * top + j)
+  const int32_t* ids;
+  const float* weights;
+  int experts, top;
+  int kw;              // waves of a workgroup, along K
+};
+
+// Two values of all lanes into one: a's sum over lanes OFF apart where lane & OFF is 0, b's where not.
+template <int OFF>
+__device__ __forceinline__ float merge(float a, float b, int lane) {
+  const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+  if constexpr (OFF == 32) {
+    const auto r = __builtin_amdgcn_permlane32_swap(ua, ub, false, false);
+    return __uint_as_float((uint32_t)r[0]) + __uint_as_float((uint32_t)r[1]);
+  } else if constexpr (OFF == 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(ua, ub, false, false);
+    return __uint_as_float((uint32_t)r[0]) + __uint_as_float((uint32_t)r[1]);
+  } else {  // 8: a row of 16 lanes rotated by 8
+    const float keep = lane & 8 ? b : a, send = lane & 8 ? a : b;
+    return keep + __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(send), 0x128, 0xF, 0xF,
+                                                                       true));
+  }
+}
+
+__device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float c) {
+  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, a), __builtin_bit_cast(bf16x2, b), c, false);
+}
+
+// RB rows a workgroup (GATED: half of them gate rows, half their up rows); MT tokens.
+template <int MT, int RB, int MODE, int OCC>
+__global__ __launch_bounds__(512, OCC) void int4_vec_kernel(Args p) {
+  constexpr int OUT = MODE == GATED ? RB / 2 : RB;  // outputs a workgroup
+  __shared__ float red[8][RB * MT];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int kw = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int nblocks = (p.n + OUT - 1) / OUT;
+  const int64_t item = blockIdx.x / nblocks;  // PLAIN: tokens from MT item; GATED: a pair; DOWN: a token
+  const int n0 = (int)(blockIdx.x % nblocks) * OUT;
+  const int blocks = p.k / 32, chunks = (blocks + 63) / 64, groups = p.k / p.group;
+  const int gshift = p.group == 32 ? 0 : p.group == 64 ? 1 : 2;
+  const size_t half = (size_t)p.k / 2;
+  size_t expert = 0;
+  if constexpr (MODE == GATED) {
+    const int id = p.ids[item];
+    if ((uint32_t)id >= (uint32_t)p.experts) return;
+    expert = id;
+  }
+
+  float acc[RB][MT];
+#pragma unroll
+  for (int r = 0; r < RB; ++r)
+#pragma unroll
+    for (int t = 0; t < MT; ++t) acc[r][t] = 0.0f;
+
+  const int work = MODE == DOWN ? chunks * p.top : chunks;
+  for (int c = kw; c < work; c += p.kw) {
+    int chunk = c;
+    float weight = 1.0f;
+    const uint16_t* xr = p.x;
+    if constexpr (MODE == DOWN) {
+      const int slot = c / chunks;
+      chunk = c - slot * chunks;
+      const int id = p.ids[item * p.top + slot];
+      if ((uint32_t)id >= (uint32_t)p.experts) continue;  // uniform
+      expert = id;
+      weight = p.weights[item * p.top + slot];
+      xr += (size_t)(item * p.top + slot) * p.k;
+    } else if constexpr (MODE == GATED) {
+      xr += (size_t)(item / p.top) * p.k;
+    }
+    const int b = chunk * 64 + lane, kb = min(b, blocks - 1);
+
+    u32x4 w[RB];
+    uint32_t s[RB], z[RB];
+#pragma unroll
+    for (int r = 0; r < RB; ++r) {
+      const int col = min(n0 + (MODE == GATED ? r % OUT : r), p.n - 1) + (MODE == GATED && r >= OUT ? p.n : 0);
+      const size_t row = expert * (MODE == GATED ? 2 * (size_t)p.n : (size_t)p.n) + col;
+      w[r] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p.w.codes + row * half) + kb);
+      const size_t g = row * groups + (kb >> gshift);
+      s[r] = p.w.scales[g];
+      z[r] = p.w.zeros == nullptr ? kInt4Zero : p.w.zeros[g];
+    }
+    uint32_t x[MT][16];
+    float sx[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      const size_t tok = MODE == PLAIN ? min(item * MT + t, (int64_t)p.m - 1) : 0;
+      const u32x4* xp = reinterpret_cast<const u32x4*>(xr + tok * p.k + (size_t)kb * 32);
+      sx[t] = 0.0f;
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        const u32x4 v = xp[d];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[t][4 * d + i] = b < blocks ? v[i] : 0u;  // past the row: nothing is added
+          sx[t] = dot2(0x3F803F80u, x[t][4 * d + i], sx[t]);
+        }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < RB; ++r) {
+      float sum[MT];
+#pragma unroll
+      for (int t = 0; t < MT; ++t) sum[t] = 0.0f;
+#pragma unroll
+      for (int d = 0; d < 4; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t q = int4_pair(w[r][d], i);
+#pragma unroll
+          for (int t = 0; t < MT; ++t) sum[t] = dot2(q, x[t][4 * d + i], sum[t]);
+        }
+      const float scale = bf16_to_f32(s[r]) * weight, zp = 128.0f + (float)z[r];
+#pragma unroll
+      for (int t = 0; t < MT; ++t) acc[r][t] += scale * (sum[t] - zp * sx[t]);
+    }
+  }
+
+  // rows 2^0, 2^1, 2^2 go to lane bits 5, 4, 3
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    float v[RB / 2];
+#pragma unroll
+    for (int r = 0; r < RB / 2; ++r) v[r] = merge<32>(acc[2 * r][t], acc[2 * r + 1][t], lane);
+    float u = merge<16>(v[0], v[1], lane);
+    int row = (lane >> 5 & 1) | (lane >> 4 & 1) << 1;
+    uint32_t f;
+    if constexpr (RB == 8) {
+      u = merge<8>(u, merge<16>(v[2], v[3], lane), lane);
+      row |= (lane >> 3 & 1) << 2;
+      f = __float_as_uint(u);
+      f = fold_lanes<4>(fold_lanes<2>(fold_lanes<1>(f, bits_sum), bits_sum), bits_sum);
+    } else {
+      f = __float_as_uint(u);
+      f = fold_lanes<8>(fold_lanes<4>(fold_lanes<2>(fold_lanes<1>(f, bits_sum), bits_sum), bits_sum), bits_sum);
+    }
+    if ((lane & (64 / RB - 1)) == 0) red[kw][row * MT + t] = __uint_as_float(f);
+  }
+  __syncthreads();
+  if (tid < OUT * MT) {
+    const int t = tid % MT, i = tid / MT;
+    float v = 0.0f, u = 0.0f;
+    for (int z = 0; z < p.kw; ++z) {
+      v += red[z][i * MT + t];
+      if constexpr (MODE == GATED) u += red[z][(i + OUT) * MT + t];
+    }
+    if constexpr (MODE == GATED) v = silu_mul(v, u);
+    const int64_t row = MODE == PLAIN ? item * MT + t : item;
+    if (n0 + i < p.n && (MODE != PLAIN || row < p.m))
+      p.y[(size_t)row * p.n + n0 + i] = (uint16_t)f32x2_to_bf16x2(v, 0.0f);
+  }
+}
+
+template <int MT, int RB, int MODE, int OCC>
+hipError_t launch(Args a, int64_t items, hipStream_t s) {
+  constexpr int OUT = MODE == GATED ? RB / 2 : RB;
+  const int work = (a.k / 32 + 63) / 64 * (MODE == DOWN ? a.top : 1);
+  a.kw = work < 8 ? work : 8;
+  const int64_t grid = items * ((a.n + OUT - 1) / OUT);
+  if (grid * 64 * a.kw >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;  // HIP counts threads in 32 bits
+  hipLaunchKernelGGL((int4_vec_kernel<MT, RB, MODE, OCC>), dim3((uint32_t)grid), dim3(64 * a.kw), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_int4_vec(const Int4Gemm& g, hipStream_t s) {
+  const Args a{g.m, g.n, g.k, g.group, g.x, g.w, g.y, nullptr, nullptr, 1, 1, 0};
+  if (g.m == 1) return launch<1, 8, PLAIN, 5>(a, 1, s);
+  if (g.m == 2) return launch<2, 8, PLAIN, 4>(a, 1, s);
+  return launch<4, 4, PLAIN, 4>(a, (g.m + 3) / 4, s);
+}
+
+hipError_t launch_int4_vec_experts(const Int4Experts& e, const int32_t* ids, const float* weights, uint16_t* y,
+                                   hipStream_t s) {
+  const Args gated{0, e.f, e.d, e.group, e.x, e.gu, e.h, ids, weights, e.pairs.experts, e.pairs.top, 0};
+  const hipError_t st = launch<1, 8, GATED, 5>(gated, e.pairs.count, s);
+  if (st != hipSuccess) return st;
+  const Args down{0, e.d, e.f, e.group, e.h, e.down, y, ids, weights, e.pairs.experts, e.pairs.top, 0};
+  return launch<1, 8, DOWN, 4>(down, e.tokens, s);
+}
+
+}  // namespace sp24
