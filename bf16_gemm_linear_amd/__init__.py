@@ -35,7 +35,7 @@ __all__ = [
     "prune_compress", "decompress", "quant_fp8", "gemm", "dense_gemm", "workspace_size", "plan",
     "quant_mxfp4", "dequant_mxfp4", "gemm_mxfp4", "gated_mxfp4", "rmsnorm", "ffn_mxfp4", "ffn_mxfp4_workspace_size",
     "mxfp4_scale_index", "NORM_BF16", "NORM_FP8_ROWS", "NORM_INT8_ROWS", "NORM_FP8_GROUPS", "NORM_MXFP4",
-    "quant_int4", "dequant_int4", "gemm_int4", "pack_int4", "unpack_int4", "route", "ROUTE_SOFTMAX", "ROUTE_SIGMOID",
+    "quant_int4", "dequant_int4", "gemm_int4", "gemm_int4_workspace_size", "pack_int4", "unpack_int4", "route", "ROUTE_SOFTMAX", "ROUTE_SIGMOID",
     "experts_int4", "experts_int4_workspace_size",
     "probe_mfma_layout", "probe_mfma_rate", "probe_copy", "probe_read", "probe_ring",
 ]
@@ -122,7 +122,8 @@ _SIGS = {
     "sp24_ffn_mxfp4_workspace_size": [_i64, _i64, _i64],
     "sp24_quant_int4": [_vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp],
     "sp24_dequant_int4": [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp],
-    "sp24_gemm_int4": [_i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp],
+    "sp24_gemm_int4": [_i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
+    "sp24_gemm_int4_workspace_size": [_i64, _i64, _i64],
     "sp24_route": [ctypes.POINTER(_RouterStruct), _i64, _vp, _vp, _vp, _vp, _vp],
     "sp24_experts_int4": [ctypes.POINTER(_ExpertsStruct), _i64, _i64, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
     "sp24_experts_int4_workspace_size": [_i64, _i64, _i64, _i64, _i64],
@@ -146,6 +147,7 @@ for _name, _args in _SIGS.items():
 lib.sp24_workspace_size.restype = _sz
 lib.sp24_ffn_mxfp4_workspace_size.restype = _sz
 lib.sp24_experts_int4_workspace_size.restype = _sz
+lib.sp24_gemm_int4_workspace_size.restype = _sz
 lib.sp24_status_string.restype = ctypes.c_char_p
 
 
@@ -840,6 +842,11 @@ def unpack_int4(codes: torch.Tensor) -> torch.Tensor:
     c = codes.reshape(*codes.shape[:-1], -1, 4)
     p = torch.stack((c & 15, c >> 4), -1).reshape(*c.shape[:-1], 8)
     return p[..., [_INT4_PLACES.index(j) for j in range(8)]].reshape(*codes.shape[:-1], -1)
+
+
+def gemm_int4_workspace_size(m: int, n: int, k: int) -> int:
+    """Workspace bytes of gemm_int4 for m tokens (0 where it needs none)."""
+    return int(lib.sp24_gemm_int4_workspace_size(m, n, k))
 
 
 def experts_int4_workspace_size(tokens: int, d: int, f: int, experts: int, top: int) -> int:

@@ -20,22 +20,20 @@ namespace sp24 {
 
 constexpr uint32_t kInt4Zero = 8;  // the zero point where none are given
 
-// Pair i of a word: the bf16 (128 + q) of values 2 i and 2 i + 1 (exact: bf16 steps by 1 there).
-__device__ __forceinline__ uint32_t int4_pair(uint32_t word, int i) {
-  return ((word >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
-}
-
-// The same pair as q - z, exactly (an integer of at most 8 bits); zp = 128 + z.
-__device__ __forceinline__ uint32_t int4_pair(uint32_t word, int i, float zp) {
-  const uint32_t p = int4_pair(word, i);
-  const float lo = __uint_as_float(p << 16) - zp, hi = __uint_as_float(p & 0xFFFF0000u) - zp;
-  return __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);  // both upper halves
-}
-
-__device__ __forceinline__ bf16x8 int4_values(uint32_t word, float zp) {
-  const u32x4 v{int4_pair(word, 0, zp), int4_pair(word, 1, zp), int4_pair(word, 2, zp), int4_pair(word, 3, zp)};
-  return __builtin_bit_cast(bf16x8, v);
-}
+// The words' constants where one instruction takes both: a vector instruction here has room for one scalar
+// register and no literal, so left to itself the compiler masks and sets in two.
+struct Int4Bits {
+  uint32_t mask, magic;
+  __device__ __forceinline__ Int4Bits() : mask(0x000F000Fu), magic(0x43004300u) {
+    asm("" : "+s"(mask));
+    asm("" : "+v"(magic));
+  }
+  // Pair i of a word: the bf16 (128 + q) of values 2 i and 2 i + 1 (exact: bf16 steps by 1 there).
+  __device__ __forceinline__ uint32_t pair(uint32_t word, int i) const { return ((word >> (4 * i)) & mask) | magic; }
+  __device__ __forceinline__ bf16x8 values(uint32_t word) const {
+    return __builtin_bit_cast(bf16x8, u32x4{pair(word, 0), pair(word, 1), pair(word, 2), pair(word, 3)});
+  }
+};
 
 // sp24_int4_quant.hip
 hipError_t launch_quant_int4(const uint16_t* w, int64_t rows, int64_t cols, int64_t group, uint8_t* codes,
@@ -65,7 +63,9 @@ struct Int4Gemm {
   Int4Weight w;
   uint16_t* y;
 };
-hipError_t launch_int4_gemm(const Int4Gemm& a, hipStream_t s);
+// part: of int4_gemm_workspace bytes.
+hipError_t launch_int4_gemm(const Int4Gemm& a, float* part, hipStream_t s);
+size_t int4_gemm_workspace(int64_t m, int64_t n, int64_t k);
 
 // The experts' products, rows being places: h[place, f] = silu(x Wg^T) (x Wu^T) of the pair's token, in
 // bf16; part[pair, d] = h[place] Wd^T, in fp32.
@@ -85,10 +85,16 @@ hipError_t launch_int4_experts(const Int4Experts& a, hipStream_t s);
 hipError_t launch_int4_vec(const Int4Gemm& g, hipStream_t s);
 hipError_t launch_int4_vec_experts(const Int4Experts& e, const int32_t* ids, const float* weights, uint16_t* y,
                                    hipStream_t s);
-// sp24_int4_stream.hip: rb row blocks of 16, 16 mb tokens and `cols` output columns a workgroup.
-hipError_t launch_int4_stream(int rb, int mb, int cols, const Int4Gemm& g, hipStream_t s);
-hipError_t launch_int4_stream_gated(int rb, int mb, int cols, const Int4Experts& e, hipStream_t s);
-hipError_t launch_int4_stream_down(int rb, int mb, int cols, const Int4Experts& e, hipStream_t s);
+constexpr int kSlabTokens = 1024;  // dense products: beyond, the tiled kernel is always the faster
+// sp24_int4_slab.hip: 16 mb tokens a workgroup, its waves along the columns (32 each; GATED: 16) and along K, the
+// values of K of a workgroup (k or more: no slices) and of a pass; multiples of 128.
+struct SlabPlan {
+  int mb, cbs, kp, slice, chunk;
+};
+// part: fp32 [slices, m, n], with slices
+hipError_t launch_int4_slab(const SlabPlan& q, const Int4Gemm& g, float* part, hipStream_t s);
+hipError_t launch_int4_slab_gated(const SlabPlan& q, const Int4Experts& e, hipStream_t s);
+hipError_t launch_int4_slab_down(const SlabPlan& q, const Int4Experts& e, hipStream_t s);
 // sp24_int4_tiled.hip: configuration cfg.
 hipError_t launch_int4_tiled(int cfg, const Int4Gemm& g, hipStream_t s);
 hipError_t launch_int4_tiled_gated(int cfg, const Int4Experts& e, hipStream_t s);
@@ -103,32 +109,46 @@ hipError_t launch_join_pairs(const float* part, const int32_t* ids, const float*
 hipError_t launch_route(const sp24_router& r, int64_t tokens, const void* logits, const float* bias, int32_t* ids,
                         float* weights, hipStream_t s);
 
-// The tile of up to BM places that tile number `tile` stands for, all experts' tiles counted one
-// after the other; false past the last.  Every lane of the wave gets the same answer.
+// Tiles of up to BM places by columns: `number` counts, expert after expert, column tile after column tile and
+// in each all of the expert's row tiles (which read the same rows of W).  False past the last.  Every lane of
+// the wave gets the same answer.
 template <int BM>
-__device__ __forceinline__ bool find_tile(const Pairs& p, int tile, int lane, int& expert, int& first, int& rows) {
+__device__ __forceinline__ bool find_tile(const Pairs& p, int number, int columns, int lane, int& expert, int& first,
+                                          int& rows, int& column) {
   int base = 0;
   for (int c = 0; c < p.experts; c += 64) {
     const int e = c + lane;
     const int lo = e < p.experts ? p.offsets[e] : 0, hi = e < p.experts ? p.offsets[e + 1] : 0;
-    int upto = (hi - lo + BM - 1) / BM;  // tiles of experts c .. e
+    int upto = (hi - lo + BM - 1) / BM * columns;  // of experts c .. e
 #pragma unroll
     for (int o = 1; o < 64; o *= 2) {
       const int v = __shfl_up(upto, o);
       if (lane >= o) upto += v;
     }
-    const uint64_t past = __ballot(tile < base + upto);
+    const uint64_t past = __ballot(number < base + upto);
     if (past != 0) {
       const int at = __ffsll((unsigned long long)past) - 1;
       const int start = at == 0 ? base : base + __shfl(upto, at - 1);
+      const int begin = __shfl(lo, at), end = __shfl(hi, at), tiles = (end - begin + BM - 1) / BM;
       expert = c + at;
-      first = __shfl(lo, at) + (tile - start) * BM;
-      rows = min(BM, __shfl(hi, at) - first);
+      column = (number - start) / tiles;
+      first = begin + (number - start - column * tiles) * BM;
+      rows = min(BM, end - first);
       return true;
     }
     base += __shfl(upto, 63);
   }
   return false;
+}
+
+// The number of such tiles.  Every lane of the wave gets the same answer.
+template <int BM>
+__device__ __forceinline__ int count_tiles(const Pairs& p, int lane) {
+  int tiles = 0;
+  for (int e = lane; e < p.experts; e += 64) tiles += (p.offsets[e + 1] - p.offsets[e] + BM - 1) / BM;
+#pragma unroll
+  for (int o = 1; o < 64; o *= 2) tiles += __shfl_xor(tiles, o);
+  return tiles;
 }
 
 // A bound of the number of such tiles that needs no look at the ids.

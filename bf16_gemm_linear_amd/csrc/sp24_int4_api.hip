@@ -69,20 +69,28 @@ int sp24_dequant_int4(const uint8_t* codes, const void* scales_bf16, const uint8
                                     static_cast<uint16_t*>(out_bf16), s), s);
 }
 
+size_t sp24_gemm_int4_workspace_size(int64_t m, int64_t n, int64_t k) {
+  return rows_ok(m) && rows_ok(n) && cols_ok(k, 32) ? int4_gemm_workspace(m, n, k) : 0;
+}
+
 int sp24_gemm_int4(int64_t m, int64_t n, int64_t k, int64_t group, const void* x_bf16, const uint8_t* codes,
-                   const void* scales_bf16, const uint8_t* zeros, void* y_bf16, void* stream) {
+                   const void* scales_bf16, const uint8_t* zeros, void* y_bf16, void* ws, size_t ws_bytes,
+                   void* stream) {
   if (!x_bf16 || !codes || !scales_bf16 || !y_bf16) return SP24_ERR_NULL;
   if (!rows_ok(m) || !rows_ok(n) || !group_ok(group) || !cols_ok(k, group)) return SP24_ERR_SHAPE;
   if (!aligned16(x_bf16) || !aligned16(codes) || !aligned16(scales_bf16) || !aligned16(zeros) || !aligned16(y_bf16))
     return SP24_ERR_ALIGN;
+  const size_t need = int4_gemm_workspace(m, n, k);
+  if (need > 0 && (ws == nullptr || ws_bytes < need)) return SP24_ERR_WORKSPACE;
+  if (need > 0 && !aligned16(ws)) return SP24_ERR_ALIGN;
   const size_t sb = scale_bytes(n, k, group);
   if (any_alias({{x_bf16, (size_t)m * k * 2}, {codes, code_bytes(n, k)}, {scales_bf16, sb}, {zeros, sb / 2}},
-                {Span{y_bf16, (size_t)m * n * 2}}))
+                {Span{y_bf16, (size_t)m * n * 2}, Span{ws, need}}))
     return SP24_ERR_ALIAS;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const Int4Gemm a{(int)m, (int)n, (int)k, (int)group, static_cast<const uint16_t*>(x_bf16),
                    Int4Weight{codes, static_cast<const uint16_t*>(scales_bf16), zeros}, static_cast<uint16_t*>(y_bf16)};
-  return finish(launch_int4_gemm(a, s), s);
+  return finish(launch_int4_gemm(a, static_cast<float*>(ws), s), s);
 }
 
 int sp24_route(const sp24_router* router, int64_t tokens, const void* logits, const float* bias_f32, int32_t* ids_out,

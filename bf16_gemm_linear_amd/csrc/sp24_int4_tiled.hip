@@ -71,7 +71,9 @@ __global__ __launch_bounds__(C::NT, C::OCC) void int4_tiled_kernel(Args p) {
 
   // Workgroups go to the 8 XCDs in turn; each XCD takes a run of tiles, all row tiles of a column
   // tile next to each other, so that its L2 holds the W and X that they share.
-  const int total = p.tiles * p.nblocks, run = (total + 7) / 8;
+  int tiles = p.tiles;
+  if constexpr (MODE != PLAIN) tiles = count_tiles<C::BM>(p.pairs, lane);  // the grid is for the most there can be
+  const int total = tiles * p.nblocks, run = (total + 7) / 8;
   const int number = (int)(blockIdx.x % 8) * run + (int)(blockIdx.x / 8);
   if ((int)(blockIdx.x / 8) >= run || number >= total) return;
   int expert = 0, first, rows, nb;
@@ -80,8 +82,7 @@ __global__ __launch_bounds__(C::NT, C::OCC) void int4_tiled_kernel(Args p) {
     nb = number / p.tiles;
     rows = min(C::BM, p.m - first);
   } else {
-    nb = number % p.nblocks;
-    if (!find_tile<C::BM>(p.pairs, number / p.nblocks, lane, expert, first, rows)) return;
+    if (!find_tile<C::BM>(p.pairs, number, p.nblocks, lane, expert, first, rows, nb)) return;
   }
   const int n0 = nb * (C::BN / H);
 

@@ -70,6 +70,7 @@ __global__ __launch_bounds__(512, OCC) void int4_vec_kernel(Args p) {
     expert = id;
   }
 
+  const Int4Bits bits;
   float acc[RB][MT];
 #pragma unroll
   for (int r = 0; r < RB; ++r)
@@ -131,7 +132,7 @@ __global__ __launch_bounds__(512, OCC) void int4_vec_kernel(Args p) {
       for (int d = 0; d < 4; ++d)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t q = int4_pair(w[r][d], i);
+          const uint32_t q = bits.pair(w[r][d], i);
 #pragma unroll
           for (int t = 0; t < MT; ++t) sum[t] = dot2(q, x[t][4 * d + i], sum[t]);
         }

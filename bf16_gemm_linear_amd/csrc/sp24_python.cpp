@@ -328,15 +328,17 @@ PyObject* dequant_int4(PyObject* const* a) {  // codes, scales, zeros, out
   return THPVariable_Wrap(out);
 }
 
-PyObject* gemm_int4(PyObject* const* a) {  // x, codes, scales, zeros, out
+PyObject* gemm_int4(PyObject* const* a) {  // x, codes, scales, zeros, out, ws
   const Tensor& x = need(a[0], "x", {at::kBFloat16}, 2, nullptr);
   const at::Device d = x.device();
   const Weight4 w = weight4(a[1], a[2], a[3], "codes", 2, &d);
   if (w.cols != x.size(1))
     fail(PyExc_ValueError, "w has %lld columns, x has %lld", (long long)w.cols, (long long)x.size(1));
   const Tensor out = output(a[4], "out", {at::kBFloat16}, {x.size(0), w.rows}, d);
+  const size_t bytes = sp24_gemm_int4_workspace_size(x.size(0), w.rows, w.cols);
+  const Tensor ws = workspace(a[5], bytes, d);
   check("sp24_gemm_int4", sp24_gemm_int4(x.size(0), w.rows, w.cols, w.group, x.data_ptr(), w.codes, w.scales, w.zeros,
-                                         out.data_ptr(), stream_of(d)));
+                                         out.data_ptr(), data(ws), bytes, stream_of(d)));
   return THPVariable_Wrap(out);
 }
 
@@ -426,7 +428,7 @@ Function g_ffn{"ffn_mxfp4", ffn, 6, 11,
                 "residual_out", "ws"}};
 Function g_quant4{"quant_int4", quant_int4, 1, 6, {"w", "group", "zeros", "out", "scales_out", "zeros_out"}};
 Function g_dequant4{"dequant_int4", dequant_int4, 2, 4, {"codes", "scales", "zeros", "out"}};
-Function g_gemm4{"gemm_int4", gemm_int4, 3, 5, {"x", "codes", "scales", "zeros", "out"}};
+Function g_gemm4{"gemm_int4", gemm_int4, 3, 6, {"x", "codes", "scales", "zeros", "out", "ws"}};
 Function g_route{"route", route, 2, 11,
                  {"logits", "top", "kind", "bias", "groups", "top_groups", "group_best", "renormalise", "factor",
                   "ids", "weights"}};
@@ -560,7 +562,7 @@ from elsewhere into this order.)"),
 --
 
 The bf16 values [rows, cols] that integer 4-bit codes, scales and zero points stand for.)"),
-    method<g_gemm4>(R"(gemm_int4(x, codes, scales, zeros=None, out=None)
+    method<g_gemm4>(R"(gemm_int4(x, codes, scales, zeros=None, out=None, ws=None)
 --
 
 Y = X . W^T, X bf16 [m, k], W [n, k] in integer 4-bit with group scales; bf16 [m, n].)"),

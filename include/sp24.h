@@ -588,10 +588,16 @@ int sp24_dequant_int4(const uint8_t* codes, const void* scales_bf16, const uint8
  * groups in fp32; rounded once.  The order of the sums is fixed for a given (m, n, k):
  * results are bitwise reproducible.  A token with an Inf or a NaN has Inf or NaN in
  * its row of Y, and only there; finite values of X reach up to 2^119.
- * Requires m, n >= 1, at most 2^21; group <= k <= 2^20.  No workspace.
- * (SP24_ERR_HIP where no grid covers the outputs: beyond 2^32 of them.) */
+ * Requires m, n >= 1, at most 2^21; group <= k <= 2^20.
+ *   ws/ws_bytes: sp24_gemm_int4_workspace_size(m, n, k), which is 0 outside 3..1024 tokens.
+ * (SP24_ERR_HIP where no grid covers the outputs: beyond 2^39 of them.) */
 int sp24_gemm_int4(int64_t m, int64_t n, int64_t k, int64_t group, const void* x_bf16, const uint8_t* codes,
-                   const void* scales_bf16, const uint8_t* zeros, void* y_bf16, void* stream);
+                   const void* scales_bf16, const uint8_t* zeros, void* y_bf16, void* ws, size_t ws_bytes,
+                   void* stream);
+
+/* Workspace bytes of sp24_gemm_int4 (0 if none; also 0 for invalid sizes, which the call
+ * itself then rejects).  Host-only. */
+size_t sp24_gemm_int4_workspace_size(int64_t m, int64_t n, int64_t k);
 
 typedef enum sp24_route_kind { SP24_ROUTE_SOFTMAX = 0, SP24_ROUTE_SIGMOID = 1 } sp24_route_kind;
 

@@ -48,20 +48,26 @@ def test_quant_output_overlap():
     assert quant(z=at(2) + 16) == EALIAS
 
 
-def gemm(m=8, n=256, k=256, group=128, x=at(0), c=at(1), s=at(2), z=at(3), y=at(4)):
-    return lib.sp24_gemm_int4(m, n, k, group, p(x), p(c), p(s), p(z), p(y), None)
+def gemm(m=8, n=256, k=4096, group=128, x=at(0), c=at(1), s=at(2), z=at(3), y=at(4), ws=at(5), ws_bytes=1 << 27):
+    return lib.sp24_gemm_int4(m, n, k, group, p(x), p(c), p(s), p(z), p(y), p(ws), ws_bytes, None)
 
 
 def test_gemm_refusals():
     for name in ("x", "c", "s", "y"):
         assert gemm(**{name: None}) == ENULL
-    for name in ("x", "c", "s", "z", "y"):
+    need = sp.gemm_int4_workspace_size(8, 256, 4096)
+    assert need > 0 and gemm(ws=None) == EWS and gemm(ws_bytes=need - 1) == EWS
+    assert sp.gemm_int4_workspace_size(1, 256, 4096) == 0 and sp.gemm_int4_workspace_size(0, 256, 4096) == 0
+    assert sp.gemm_int4_workspace_size(8, 256, 100) == 0
+    for name in ("x", "c", "s", "z", "y", "ws"):
         assert gemm(**{name: at(9) + 4}) == EALIGN
     for bad in (dict(m=0), dict(n=0), dict(k=0), dict(k=192), dict(k=64), dict(group=48), dict(m=(1 << 21) + 1),
                 dict(n=(1 << 21) + 1), dict(k=(1 << 20) + 128), dict(m=-1)):
         assert gemm(**bad) == ESHAPE, bad
     for name in ("x", "c", "s", "z"):
         assert gemm(**{name: at(4) + 8 * 256 * 2 - 16}) == EALIAS, name
+        assert gemm(**{name: at(5) + need - 16}) == EALIAS, name
+    assert gemm(y=at(5)) == EALIAS
 
 
 def router(kind=0, fp32=1, experts=64, top=8, groups=1, top_groups=1, best=1, renormalise=1, factor=1.0, tokens=4,
