@@ -3,11 +3,12 @@
 //   symmetric:   s = bf16(amax / 7), q = clamp(rne(w / s), -8, 7) + 8
 //   zero points: lo = min(0, min w), hi = max(0, max w), s = bf16((hi - lo) / 15),
 //                z = clamp(rne(-lo / s), 0, 15), q = clamp(rne(w / s) + z, 0, 15)
-// with s = 1 where that is 0, and s = NaN, q = z = 8 for a group with an Inf or a NaN.  The divisions
-// are IEEE: a quotient of two bf16 values that is not a tie lies further than 2^-17 from one, so the
-// codes are those of exact arithmetic.
+// with s = 1 where that is 0, and s = NaN, q = z = 8 for a group with an Inf or a NaN.  A quotient of two
+// bf16 values that is not a tie lies further than 2^-17 of it from one, so quotients to fp32 that are exact where
+// fp32 holds them give the codes of exact arithmetic.
 //
 // A lane takes 8 values (a 16-byte load, a 4-byte store), group / 8 lanes a group.
+#include "sp24_fp8.hpp"
 #include "sp24_int4.hpp"
 #include "sp24_mx4.hpp"
 
@@ -20,13 +21,12 @@ __device__ __forceinline__ uint32_t f_max(uint32_t a, uint32_t b) {
   return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
 }
 // over the LANES neighbouring lanes of a group
-template <int LANES>
-__device__ __forceinline__ float group_max(float v) {
-  uint32_t b = __float_as_uint(v);
-  b = fold_lanes<2>(fold_lanes<1>(b, f_max), f_max);
-  if constexpr (LANES >= 8) b = fold_lanes<4>(b, f_max);
-  if constexpr (LANES >= 16) b = fold_lanes<8>(b, f_max);
-  return __uint_as_float(b);
+template <int LANES, class F>
+__device__ __forceinline__ uint32_t group_fold(uint32_t v, F f) {
+  v = fold_lanes<2>(fold_lanes<1>(v, f), f);
+  if constexpr (LANES >= 8) v = fold_lanes<4>(v, f);
+  if constexpr (LANES >= 16) v = fold_lanes<8>(v, f);
+  return v;
 }
 
 // bf16 to nearest even; finite and not negative.  Zero becomes 1: the scale of a group of zeros.
@@ -52,32 +52,44 @@ __global__ __launch_bounds__(kThreads) void int4_quant_kernel(const uint16_t* __
       v[2 * i] = __uint_as_float(d[i] << 16);
       v[2 * i + 1] = __uint_as_float(d[i] & 0xFFFF0000u);
     }
-    bool odd = false;  // Inf or NaN
-    float lo = 0.0f, hi = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      odd = odd || (__float_as_uint(v[i]) & 0x7F800000u) == 0x7F800000u;
-      lo = fminf(lo, v[i]);
-      hi = fmaxf(hi, v[i]);
-    }
-    if (odd) hi = __builtin_inff();  // fmaxf drops a NaN; an Inf passes through the maxima
-    hi = group_max<LANES>(hi);
-    const float neg = group_max<LANES>(-lo);  // -lo >= 0
-    odd = hi == __builtin_inff();
+    const uint32_t key = group_fold<LANES>(key_max8(d), bits_max);  // the largest magnitude's bits
+    const bool odd = key >= 0x7F80u;                                // Inf or NaN
     uint32_t sb;
-    float z = 8.0f;
+    float neg = 0.0f, z = 8.0f;
     if constexpr (ZEROS) {
+      float lo = 0.0f, hi = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        lo = fminf(lo, v[i]);
+        hi = fmaxf(hi, v[i]);
+      }
+      hi = __uint_as_float(group_fold<LANES>(__float_as_uint(hi), f_max));
+      neg = __uint_as_float(group_fold<LANES>(__float_as_uint(-lo), f_max));  // -lo >= 0
       const float range = hi + neg;  // beyond fp32 for the largest values: their halves are not
       sb = scale_bits(range < __builtin_inff() ? range / 15.0f : (0.5f * hi + 0.5f * neg) / 7.5f);
     } else {
-      sb = scale_bits(fmaxf(hi, neg) / 7.0f);
+      sb = scale_bits(__uint_as_float(key << 16) / 7.0f);
     }
     const float s = __uint_as_float(sb << 16);
     if constexpr (ZEROS) z = fminf(rintf(neg / s), 15.0f);
+    float t[8];
+    if (s > 0x1p-60f && s < 0x1p60f) {
+      // w r and one correction with the exact remainder: what is a tie comes out exactly, and the rest
+      // lies too far from one for the last bit to matter
+      const float r = 1.0f / s;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float a = v[i] * r;
+        t[i] = fmaf(fmaf(-a, s, v[i]), r, a);
+      }
+    } else {  // r or the remainder can leave fp32's range
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t[i] = v[i] / s;
+    }
     uint32_t q = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      float c = rintf(v[i] / s);
+      float c = rintf(t[i]);
       if constexpr (ZEROS) c = fminf(fmaxf(c + z, 0.0f), 15.0f);
       else c = fminf(fmaxf(c, -8.0f), 7.0f) + 8.0f;
       q |= (uint32_t)c << (4 * (i / 2) + 16 * (i % 2));

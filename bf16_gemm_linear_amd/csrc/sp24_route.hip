@@ -6,185 +6,313 @@
 //   the order of the indices, and with a -inf its weight is 0.
 // Scores that are compared (with a bias, or summed for a group) are formed in 64 bits: among hundreds of
 // experts two fp32 scores within a rounding of each other are met every few thousand tokens, and the
-// choice would depend on the rounding.
+// choice would depend on the rounding.  Without them the logits are compared, in fp32, as they are.
 //
-// A wave takes a token, lane l the experts l, l + 64, ...
+// A wave takes a token.  The lanes are dealt to the groups, a power of two to each, and a lane holds V
+// neighbouring experts of its group, so that a group's value is a reduction over its lanes, all groups at
+// once, and the lowest lane that holds a value has the lowest index.  An expert that was taken, or is in no chosen
+// group, is NaN, which maxima pass over.  Reductions are register exchanges (sp24_mx4.hpp's).  The weights are
+// formed by the first `top` lanes, each from its expert's logit, in 64 bits.
 #include "sp24_int4.hpp"
+#include "sp24_mx4.hpp"
 
 namespace sp24 {
 namespace {
 
-constexpr double kNone = -__builtin_inf();
+constexpr float kMaxLogit = 3.402823466e38f;  // +inf counts as this
 
-__device__ __forceinline__ double wave_max(double v) {
-#pragma unroll
-  for (int o = 1; o < 64; o *= 2) v = fmax(v, __shfl_xor(v, o));
-  return v;
-}
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int o = 1; o < 64; o *= 2) v += __shfl_xor(v, o);
-  return v;
-}
-// The largest value of the wave and the lowest index that has it.
-__device__ __forceinline__ void wave_best(double& v, int& i) {
-#pragma unroll
-  for (int o = 1; o < 64; o *= 2) {
-    const double w = __shfl_xor(v, o);
-    const int j = __shfl_xor(i, o);
-    if (w > v || (w == v && j < i)) {
-      v = w;
-      i = j;
+// The value of the lane OFF away (for 4 and 8 one of the aligned group of OFF lanes there).
+template <int OFF, class T>
+__device__ __forceinline__ void pair_of(T v, T& a, T& b) {
+  if constexpr (sizeof(T) == 8) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    uint32_t l0, l1, h0, h1;
+    pair_of<OFF>((uint32_t)u, l0, l1);
+    pair_of<OFF>((uint32_t)(u >> 32), h0, h1);
+    a = __builtin_bit_cast(T, (uint64_t)h0 << 32 | l0);
+    b = __builtin_bit_cast(T, (uint64_t)h1 << 32 | l1);
+  } else {
+    const uint32_t u = __builtin_bit_cast(uint32_t, v);
+    if constexpr (OFF == 32) {
+      const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+      a = __builtin_bit_cast(T, (uint32_t)r[0]);
+      b = __builtin_bit_cast(T, (uint32_t)r[1]);
+    } else if constexpr (OFF == 16) {
+      const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+      a = __builtin_bit_cast(T, (uint32_t)r[0]);
+      b = __builtin_bit_cast(T, (uint32_t)r[1]);
+    } else {
+      constexpr int CTRL = OFF == 1 ? 0xB1 : OFF == 2 ? 0x4E : OFF == 4 ? 0x141 : 0x140;
+      a = v;
+      b = __builtin_bit_cast(T, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, CTRL, 0xF, 0xF, true));
     }
   }
 }
+__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }  // not the NaN
+__device__ __forceinline__ double larger(double a, double b) { return fmax(a, b); }
 
-// NV values a lane: experts <= 64 NV.
-template <int NV, bool BF16>
-__global__ __launch_bounds__(256) void route_kernel(sp24_router r, int64_t tokens, const void* __restrict__ logits,
-                                                    const float* __restrict__ bias, int32_t* __restrict__ ids,
-                                                    float* __restrict__ weights) {
+template <int OFF, class T>
+__device__ __forceinline__ T step_max(T v) {
+  T a, b;
+  pair_of<OFF>(v, a, b);
+  return larger(a, b);
+}
+template <class T>
+__device__ __forceinline__ T wave_max(T v) {
+  return step_max<32>(step_max<16>(step_max<8>(step_max<4>(step_max<2>(step_max<1>(v))))));
+}
+template <int OFF, class T>
+__device__ __forceinline__ T step_sum(T v) {
+  T a, b;
+  pair_of<OFF>(v, a, b);
+  return a + b;
+}
+template <class T>
+__device__ __forceinline__ T wave_sum(T v) {
+  return step_sum<32>(step_sum<16>(step_sum<8>(step_sum<4>(step_sum<2>(step_sum<1>(v))))));
+}
+// the two largest
+template <int OFF, class T>
+__device__ __forceinline__ void step_two(T& best, T& second) {
+  T a, b, c, d;
+  pair_of<OFF>(best, a, b);
+  pair_of<OFF>(second, c, d);
+  best = larger(a, b);
+  second = larger(a < b ? a : b, larger(c, d));
+}
+
+// e^x to about 2^-51, x <= 0 (below -745: 0; NaN stays one): x = k ln 2 + r, the series of e^r to its
+// fourteenth term (|r| <= 0.347: the next is below 2^-57).
+__device__ __forceinline__ double exp_of(double x) {
+  const double k = rint(x * 1.4426950408889634);
+  double r = fma(k, -6.93147182464599609e-01, x);  // ln 2 as the nearest float (k times it is exact) and the rest
+  r = fma(k, 1.90465429995776805e-09, r);
+  double p = 1.0 / 6227020800.0;
+  p = fma(p, r, 1.0 / 479001600.0);
+  p = fma(p, r, 1.0 / 39916800.0);
+  p = fma(p, r, 1.0 / 3628800.0);
+  p = fma(p, r, 1.0 / 362880.0);
+  p = fma(p, r, 1.0 / 40320.0);
+  p = fma(p, r, 1.0 / 5040.0);
+  p = fma(p, r, 1.0 / 720.0);
+  p = fma(p, r, 1.0 / 120.0);
+  p = fma(p, r, 1.0 / 24.0);
+  p = fma(p, r, 1.0 / 6.0);
+  p = fma(p, r, 0.5);
+  p = fma(p, r, 1.0);
+  p = fma(p, r, 1.0);
+  return x < -745.0 ? 0.0 : __builtin_amdgcn_ldexp(p, (int)fmax(k, -2000.0));
+}
+// sigmoid, from e^-|x|
+__device__ __forceinline__ double sigmoid(double x) {
+  const double e = exp_of(-fabs(x));
+  return (x < 0.0 ? e : 1.0) / (1.0 + e);
+}
+
+struct Shape {
+  int experts, top, groups, per, lanes_log2;  // per: experts of a group; 2^lanes_log2 lanes hold it
+};
+
+// T: double where scores are compared, float where logits are.
+template <class T, int V, bool BF16>
+__global__ __launch_bounds__(256) void route_kernel(sp24_router r, Shape s, int64_t tokens,
+                                                    const void* __restrict__ logits, const float* __restrict__ bias,
+                                                    int32_t* __restrict__ ids, float* __restrict__ weights) {
+  constexpr bool WIDE = sizeof(T) == 8;
+  const float none = -__builtin_inff();
+  const T gone = __builtin_nanf("");
   const int lane = threadIdx.x & 63;
   const int64_t t = (int64_t)blockIdx.x * 4 + threadIdx.x / 64;
   if (t >= tokens) return;  // whole waves
-  const int E = (int)r.experts;
   const bool soft = r.kind == SP24_ROUTE_SOFTMAX;
-  double l[NV], score[NV], c[NV];
-  double top = kNone;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int e = lane + 64 * i;
-    l[i] = kNone;
-    if (e < E) {
-      l[i] = BF16 ? (double)bf16_to_f32(static_cast<const uint16_t*>(logits)[t * E + e])
-                  : (double)static_cast<const float*>(logits)[t * E + e];
-      l[i] = l[i] > 3.4028234663852886e38 ? 3.4028234663852886e38 : l[i];  // +inf: the largest number
-      top = fmax(top, l[i]);  // drops a NaN
-    }
-  }
-  top = wave_max(top);
-  double sum = 0.0;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    // -inf: 0, also where all of them are; NaN stays one
-    score[i] = l[i] == kNone ? 0.0 : soft ? exp(l[i] - top) : 1.0 / (1.0 + exp(-l[i]));
-    sum += score[i];
-  }
-  if (soft) {
-    sum = wave_sum(sum);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) score[i] = sum == 0.0 ? 0.0 : score[i] / sum;
-  }
-  bool taken[NV];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int e = lane + 64 * i;
-    taken[i] = e >= E;
-    c[i] = !(l[i] > kNone) ? kNone : bias != nullptr && e < E ? score[i] + (double)bias[e] : l[i];
-    if (c[i] != c[i]) c[i] = kNone;  // a bias or a sum that is NaN
-  }
+  const int group = lane >> s.lanes_log2, in = (lane & ((1 << s.lanes_log2) - 1)) * V;
+  const int e0 = group * s.per + in;                                    // this lane's experts: e0 .. e0 + held - 1
+  const int held = group < s.groups ? max(0, min(V, s.per - in)) : 0;
+  const int64_t row = t * s.experts;
 
-  if (r.groups > 1) {
-    // a group's value: the sum of its best one or two; the best top_groups groups stay
-    const int per = E / (int)r.groups;
-    const bool scores = bias == nullptr && r.group_best == 2;
-    double value = kNone;  // of group `lane`; groups <= 64
-    for (int g = 0; g < r.groups; ++g) {
-      double best = kNone, second = kNone;
+  float l[V];
+  if (V % 4 == 0 && s.per % 4 == 0) {  // then so are the row and held
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int e = lane + 64 * i;
-        if (e < g * per || e >= (g + 1) * per || c[i] == kNone) continue;
-        const double v = scores ? score[i] : c[i];
-        second = fmax(second, fmin(best, v));
-        best = fmax(best, v);
+    for (int i = 0; i < V; i += 4) {
+      f32x4 v{none, none, none, none};
+      if (i < held) {
+        if constexpr (BF16) {
+          const u32x2 u = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(logits) + row + e0 + i);
+          v = f32x4{__uint_as_float(u[0] << 16), __uint_as_float(u[0] & 0xFFFF0000u), __uint_as_float(u[1] << 16),
+                    __uint_as_float(u[1] & 0xFFFF0000u)};
+        } else {
+          v = *reinterpret_cast<const f32x4*>(static_cast<const float*>(logits) + row + e0 + i);
+        }
       }
 #pragma unroll
-      for (int o = 1; o < 64; o *= 2) {
-        const double b2 = __shfl_xor(best, o), s2 = __shfl_xor(second, o);
-        second = fmax(fmax(second, s2), fmin(best, b2));
-        best = fmax(best, b2);
-      }
-      if (r.group_best == 2 && second > kNone) best += second;
-      if (lane == g) value = best;
+      for (int j = 0; j < 4; ++j)
+        if (i + j < V) l[i + j] = v[j];
     }
-    uint64_t keep = 0;
-    bool used = lane >= r.groups;
-    for (int j = 0; j < r.top_groups; ++j) {
-      double v = used ? kNone : value;
-      int g = used ? 1 << 20 : lane;
-      wave_best(v, g);
-      keep |= (uint64_t)1 << g;
-      used = used || lane == g;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      l[i] = none;
+      if (i < held)
+        l[i] = BF16 ? bf16_to_f32(static_cast<const uint16_t*>(logits)[row + e0 + i])
+                    : static_cast<const float*>(logits)[row + e0 + i];
+    }
+  }
+  float most = none;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    l[i] = l[i] > kMaxLogit ? kMaxLogit : l[i];
+    most = fmaxf(most, l[i]);  // passes over a NaN
+  }
+  if (soft) most = wave_max(most);
+  // a row without numbers has no e^(l - most); its scores are 0 (or NaN)
+  const float from = most == none ? 0.0f : most;
+
+  T c[V];
+  double sum = 1.0;  // of e^(l - most), for the softmax
+  T best = none, second = none;
+  if constexpr (WIDE) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) c[i] = l[i] == none ? 0.0 : soft ? exp_of((double)l[i] - from) : sigmoid((double)l[i]);
+    if (soft) {
+      sum = 0.0;
+#pragma unroll
+      for (int i = 0; i < V; ++i) sum += c[i];
+      sum = wave_sum(sum);
+#pragma unroll
+      for (int i = 0; i < V; ++i) c[i] = sum == 0.0 ? 0.0 : c[i] / sum;
     }
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int e = lane + 64 * i;
-      if (e < E) taken[i] = (keep >> (e / per) & 1) == 0;
+    for (int i = 0; i < V; ++i) {
+      const double score = c[i];
+      c[i] = bias != nullptr && i < held ? score + (double)bias[e0 + i] : (double)l[i];
+      if (!(l[i] > none) || c[i] != c[i]) c[i] = none;  // masked
+      // the group's value is of choices, without a bias of scores
+      const double v = bias != nullptr ? c[i] : score;
+      if (c[i] != none && v == v) {
+        second = larger(second, best < v ? best : v);
+        best = larger(best, v);
+      }
+      if (i >= held) c[i] = gone;
+    }
+  } else {
+    if (soft && !r.renormalise) {
+      // e^x for x far below 0 is inexact in proportion to x, and adds as little
+      float f = 0.0f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) f += __builtin_amdgcn_exp2f((l[i] - from) * 1.4426950408889634f);
+      sum = (double)wave_sum(f);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      c[i] = l[i] > none ? l[i] : none;
+      best = larger(best, c[i]);
+      if (i >= held) c[i] = gone;
     }
   }
 
-  // slot j's expert and score end in lane j (top <= 64)
+  if (s.groups > 1) {
+    // over the group's lanes, step by step
+    if (s.lanes_log2 > 0) step_two<1>(best, second);
+    if (s.lanes_log2 > 1) step_two<2>(best, second);
+    if (s.lanes_log2 > 2) step_two<4>(best, second);
+    if (s.lanes_log2 > 3) step_two<8>(best, second);
+    if (s.lanes_log2 > 4) step_two<16>(best, second);
+    T value = best;
+    if (WIDE && r.group_best == 2 && second > none) value += second;
+    int before = 0;  // groups that come before this lane's
+    for (int g = 0; g < s.groups; ++g) {
+      T v;
+      if constexpr (WIDE) {
+        const uint64_t u = __builtin_bit_cast(uint64_t, value);
+        const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)u, g << s.lanes_log2);
+        const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)(u >> 32), g << s.lanes_log2);
+        v = __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+      } else {
+        v = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(value), g << s.lanes_log2));
+      }
+      before += v > value || (v == value && g < group);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (before >= r.top_groups) c[i] = gone;
+  }
+
+  // slot j's expert ends in lane j (top <= 64)
   int id = 0;
-  double won = 0.0, at = kNone;
-  for (int j = 0; j < r.top; ++j) {
-    double v = kNone;
-    int e = 1 << 20;
+  for (int j = 0; j < s.top; ++j) {
+    T v = c[0];
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (!taken[i] && (e == 1 << 20 || c[i] > v)) {
-        v = c[i];
-        e = lane + 64 * i;
-      }
-    wave_best(v, e);
-    double sc = 0.0, lv = kNone;
+    for (int i = 1; i < V; ++i) v = larger(v, c[i]);
+    v = wave_max(v);
+    int at = V;  // the first of this lane's with that value
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (e == lane + 64 * i) {
-        taken[i] = true;
-        sc = score[i];
-        lv = l[i];
-      }
-    sc = __shfl(sc, e & 63);
-    lv = __shfl(lv, e & 63);
-    if (lane == j) {
-      id = e;
-      won = sc;
-      at = lv;
-    }
+    for (int i = V - 1; i >= 0; --i)
+      if (c[i] == v) at = i;
+    const int winner = __ffsll((unsigned long long)__ballot(at < V)) - 1;
+    const int e = __builtin_amdgcn_readlane(e0 + at, winner);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (lane == winner && i == at) c[i] = gone;
+    if (lane == j) id = e;
+  }
+
+  double won = 0.0;
+  float at = none;
+  const bool mine = lane < s.top;
+  if (mine)
+    at = BF16 ? bf16_to_f32(static_cast<const uint16_t*>(logits)[row + id])
+              : static_cast<const float*>(logits)[row + id];
+  at = at > kMaxLogit ? kMaxLogit : at;
+  if (soft) {
+    // renormalised: relative to the largest that was chosen, so that none of them underflows
+    const float big = r.renormalise ? wave_max(at) : from;
+    won = mine && at != none ? exp_of((double)at - (big == none ? 0.0f : big)) / (sum == 0.0 ? 1.0 : sum) : 0.0;
+    if (r.renormalise) won = mine && at != none ? exp_of((double)at - (big == none ? 0.0f : big)) : 0.0;
+  } else {
+    won = mine && at != none ? sigmoid((double)at) : 0.0;
   }
   if (r.renormalise) {
-    if (soft) {  // relative to the largest that was chosen: none of them underflows
-      const double big = wave_max(at);  // drops a NaN
-      won = lane < r.top ? (at == kNone ? 0.0 : exp(at - big)) : 0.0;
-    }
-    const double all = wave_sum(lane < r.top ? won : 0.0);
+    const double all = wave_sum(won);
     won = all == 0.0 ? 0.0 : won / all;
   }
-  if (lane < r.top) {
-    ids[t * r.top + lane] = id;
-    weights[t * r.top + lane] = (float)(won * (double)r.factor);
+  if (mine) {
+    ids[t * s.top + lane] = id;
+    weights[t * s.top + lane] = (float)(won * (double)r.factor);
   }
 }
 
-template <int NV>
-hipError_t launch(const sp24_router& r, int64_t tokens, const void* logits, const float* bias, int32_t* ids,
-                  float* weights, hipStream_t s) {
+template <class T, int V>
+hipError_t launch(const sp24_router& r, const Shape& p, int64_t tokens, const void* logits, const float* bias,
+                  int32_t* ids, float* weights, hipStream_t s) {
   const dim3 grid((uint32_t)((tokens + 3) / 4)), block(256);
   if (r.logits_fp32)
-    hipLaunchKernelGGL((route_kernel<NV, false>), grid, block, 0, s, r, tokens, logits, bias, ids, weights);
+    hipLaunchKernelGGL((route_kernel<T, V, false>), grid, block, 0, s, r, p, tokens, logits, bias, ids, weights);
   else
-    hipLaunchKernelGGL((route_kernel<NV, true>), grid, block, 0, s, r, tokens, logits, bias, ids, weights);
+    hipLaunchKernelGGL((route_kernel<T, V, true>), grid, block, 0, s, r, p, tokens, logits, bias, ids, weights);
   return hipGetLastError();
+}
+
+template <class T>
+hipError_t by_size(const sp24_router& r, const Shape& p, int64_t tokens, const void* logits, const float* bias,
+                   int32_t* ids, float* weights, hipStream_t s) {
+  const int v = (p.per + (1 << p.lanes_log2) - 1) >> p.lanes_log2;  // at most 32: 31 experts a lane of 33 groups
+  if (v <= 1) return launch<T, 1>(r, p, tokens, logits, bias, ids, weights, s);
+  if (v <= 2) return launch<T, 2>(r, p, tokens, logits, bias, ids, weights, s);
+  if (v <= 4) return launch<T, 4>(r, p, tokens, logits, bias, ids, weights, s);
+  if (v <= 8) return launch<T, 8>(r, p, tokens, logits, bias, ids, weights, s);
+  if (v <= 16) return launch<T, 16>(r, p, tokens, logits, bias, ids, weights, s);
+  return launch<T, 32>(r, p, tokens, logits, bias, ids, weights, s);
 }
 
 }  // namespace
 
 hipError_t launch_route(const sp24_router& r, int64_t tokens, const void* logits, const float* bias, int32_t* ids,
                         float* weights, hipStream_t s) {
-  if (r.experts <= 64) return launch<1>(r, tokens, logits, bias, ids, weights, s);
-  if (r.experts <= 256) return launch<4>(r, tokens, logits, bias, ids, weights, s);
-  return launch<16>(r, tokens, logits, bias, ids, weights, s);
+  Shape p{(int)r.experts, (int)r.top, (int)r.groups, (int)(r.experts / r.groups), 6};
+  while (p.groups << p.lanes_log2 > 64) --p.lanes_log2;
+  const bool wide = bias != nullptr || (r.groups > 1 && r.group_best == 2);
+  return wide ? by_size<double>(r, p, tokens, logits, bias, ids, weights, s)
+              : by_size<float>(r, p, tokens, logits, bias, ids, weights, s);
 }
 
 }  // namespace sp24
