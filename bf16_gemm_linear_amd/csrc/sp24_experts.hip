@@ -6,39 +6,38 @@
 namespace sp24 {
 namespace {
 
-constexpr int kSortThreads = 256;
+constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
 
 // Workgroup e finds the places of expert e: it counts the ids below e (where its range begins) and lists
-// the pairs with id e, in their order.  A thread takes a run of neighbouring pairs, so the order holds
-// without atomics.
+// the pairs with id e, in their order, without atomics: a wave takes a run of neighbouring pairs, 64 at a
+// time, counts its own in a first pass and, behind the waves before it, places them in a second.
 __global__ __launch_bounds__(kSortThreads) void sort_pairs_kernel(const int32_t* __restrict__ ids, int count,
                                                                   int experts, int* __restrict__ offsets,
                                                                   int* __restrict__ order) {
-  __shared__ int sums[kSortThreads / 64][2];
+  __shared__ int sums[kSortWaves][2];
   const int e = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int run = (count + kSortThreads - 1) / kSortThreads;
-  const int from = min(count, tid * run), to = min(count, from + run);
+  const int run = (count + kSortThreads - 1) / kSortThreads * 64;
+  const int from = wave * run, to = min(count, from + run);
   int below = 0, mine = 0;
-  for (int i = from; i < to; ++i) {
+#pragma unroll 4
+  for (int i = from + lane; i < to; i += 64) {
     const int id = ids[i];
     below += id >= 0 && id < e;
     mine += id == e;
   }
-  int upto = mine;
 #pragma unroll
   for (int o = 1; o < 64; o *= 2) {
-    const int v = __shfl_up(upto, o), b = __shfl_xor(below, o);
-    if (lane >= o) upto += v;
-    below += b;
+    below += __shfl_xor(below, o);
+    mine += __shfl_xor(mine, o);
   }
-  if (lane == 63) {
-    sums[wave][0] = upto;
+  if (lane == 0) {
+    sums[wave][0] = mine;
     sums[wave][1] = below;
   }
   __syncthreads();
   int start = 0, before = 0, all = 0;
 #pragma unroll
-  for (int w = 0; w < kSortThreads / 64; ++w) {
+  for (int w = 0; w < kSortWaves; ++w) {
     start += sums[w][1];
     before += w < wave ? sums[w][0] : 0;
     all += sums[w][0];
@@ -47,9 +46,13 @@ __global__ __launch_bounds__(kSortThreads) void sort_pairs_kernel(const int32_t*
     offsets[e] = start;
     if (e == experts - 1) offsets[experts] = start + all;
   }
-  int at = start + before + upto - mine;
-  for (int i = from; i < to; ++i)
-    if (ids[i] == e) order[at++] = i;
+  int at = start + before;
+  for (int i0 = from; i0 < to; i0 += 64) {
+    const int i = i0 + lane;
+    const uint64_t here = __ballot(i < to && ids[min(i, count - 1)] == e);
+    if (here >> lane & 1) order[at + __popcll(here & (((uint64_t)1 << lane) - 1))] = i;
+    at += __popcll(here);
+  }
 }
 
 // y[t] = sum over slots of weight * part, in the order of the slots; 4 columns a thread (d % 32 == 0).

@@ -151,7 +151,8 @@ int sp24_experts_int4(const sp24_int4_experts* w, int64_t tokens, int64_t top, c
                       Int4Weight{w->down_codes, static_cast<const uint16_t*>(w->down_scales_bf16), w->down_zeros},
                       reinterpret_cast<uint16_t*>(b + e.h), part};
   uint16_t* const y = static_cast<uint16_t*>(y_bf16);
-  if (tokens <= 4) return finish(launch_int4_vec_experts(a, ids, weights_f32, y, s), s);
+  if (int4_experts_by_pairs(tokens, tokens * top, E, d, f))
+    return finish(launch_int4_vec_experts(a, ids, weights_f32, y, s), s);
   hipError_t st = launch_sort_pairs(ids, tokens * top, (int)E, offsets, order, s);
   if (st == hipSuccess) st = launch_int4_experts(a, s);
   if (st == hipSuccess)

@@ -56,13 +56,6 @@ double tiled_plan(int64_t m, int64_t n, int64_t k, int& cfg) {
   return t0 < t2 ? t0 : t2;
 }
 
-// X's and the scales' share of LDS left for two workgroups a CU (experts) or one.
-int fit(int k, int rows, int wrows, int group, int slice) {
-  const int c = slab_chunk(rows, wrows, group);
-  const int len = slice < k ? slice : k;
-  return len < c ? len : c;
-}
-
 }  // namespace
 
 size_t int4_gemm_workspace(int64_t m, int64_t n, int64_t k) {
@@ -79,16 +72,30 @@ hipError_t launch_int4_gemm(const Int4Gemm& a, float* part, hipStream_t s) {
   if (a.m <= kSlabTokens) {
     SlabPlan q;
     if (slab_plan(a.m, a.n, a.k, q) <= tiled) {
-      q.chunk = fit(a.k, a.m < 16 * q.mb ? a.m : 16 * q.mb, 32 * q.cbs, a.group, q.slice);
+      const int fits = slab_chunk(a.m < 16 * q.mb ? a.m : 16 * q.mb, 32 * q.cbs, a.group);
+      q.chunk = q.slice < fits ? q.slice : fits;
       return launch_int4_slab(q, a, part, s);
     }
   }
   return launch_int4_tiled(cfg, a, s);
 }
 
+bool int4_experts_by_pairs(int64_t tokens, int64_t pairs, int64_t experts, int64_t d, int64_t f) {
+  const int64_t used = pairs < experts ? pairs : experts;
+  return tokens <= 4 && (double)(pairs - used) * d * f * 1.5 <= 50e6;
+}
+
+// Pairs an expert, 64 experts of 4096 x 1792, 8 a token, gated and down in us:
+//              slab, tiles of 16   slab, tiles of 32   128 x 128 tiles   256 x 256 tiles
+//   8 (64)        126 + 69            161 + 82            394 + 202
+//   16 (128)      182 + 95            186 + 106           397 + 208
+//   37 (300)      -                   329 + 167           289 + 167         352 + 198
+//   75 (600)      -                   571 + 279           349 + 210         376 + 221
+//   150 (1200)    -                   1049 + 498          532 + 332         467 + 312
+//   222 (1777)    -                   1515 + 691          718 + 445         619 + 407
 hipError_t launch_int4_experts(const Int4Experts& a, hipStream_t s) {
   const int64_t each = a.pairs.count / a.pairs.experts;  // pairs of an expert
-  if (each <= 150) {
+  if (each <= 28) {
     SlabPlan q;
     q.mb = each <= 12 ? 1 : 2;
     const int fits = 2048 / q.mb;  // 64 KB of X: two workgroups a CU
@@ -98,12 +105,15 @@ hipError_t launch_int4_experts(const Int4Experts& a, hipStream_t s) {
     q.chunk = a.d < fits ? a.d : fits;
     const hipError_t e = launch_int4_slab_gated(q, a, s);
     if (e != hipSuccess) return e;
+    q.cbs = 8;
+    q.kp = 1;
     q.slice = a.f;
     q.chunk = a.f < fits ? a.f : fits;
     return launch_int4_slab_down(q, a, s);
   }
-  const hipError_t e = launch_int4_tiled_gated(2, a, s);
-  return e != hipSuccess ? e : launch_int4_tiled_down(2, a, s);
+  const int cfg = each <= 110 ? 2 : 0;
+  const hipError_t e = launch_int4_tiled_gated(cfg, a, s);
+  return e != hipSuccess ? e : launch_int4_tiled_down(cfg, a, s);
 }
 
 }  // namespace sp24

@@ -16,6 +16,8 @@
 // v_mfma_f32_32x32x16_bf16, A = X, B = W: lane l holds row l % 32 and values 8 (l / 32) .. + 7;
 // accumulator register 4 g + e is token 8 g + 4 (l / 32) + e, W row l % 32.  LDS rows of 128 bytes are
 // XOR-swizzled in pieces of 16; the swizzle of X is applied on the global side.
+#include <type_traits>
+
 #include "sp24_dma.hpp"
 #include "sp24_int4.hpp"
 #include "sp24_mx4.hpp"
@@ -60,9 +62,10 @@ __device__ __forceinline__ u32x4 widen(uint32_t w, float s, float ns) {
                f32x2_to_bf16x2(f(e, 1), f(e, 3)), f32x2_to_bf16x2(f(o, 1), f(o, 3))};
 }
 
-template <class C, int MODE>
+template <class C, int MODE, int G>
 __global__ __launch_bounds__(C::NT, C::OCC) void int4_tiled_kernel(Args p) {
   constexpr int TI = C::TI, TJ = C::TJ, H = MODE == GATED ? 2 : 1;
+  static_assert(C::WS % 2 == 0, "a step's number and its copy's are even together");
   static_assert(MODE != GATED || TJ == 2, "a wave's gate tile and its up tile");
   __shared__ __attribute__((aligned(16))) uint8_t lds[C::LDS];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -96,7 +99,8 @@ __global__ __launch_bounds__(C::NT, C::OCC) void int4_tiled_kernel(Args p) {
     xrow[j] = p.x + row * p.k;
   }
   // W: this thread has half `wh` (32 values of a step) of LDS row wr
-  const int groups = p.k / p.group, gshift = p.group == 32 ? 5 : p.group == 64 ? 6 : 7;
+  const int groups = p.k / G;
+  constexpr int gshift = G == 32 ? 5 : G == 64 ? 6 : 7;
   const int wh = tid & 1, wr = tid / 2;
   size_t wrow;
   {
@@ -181,75 +185,91 @@ __global__ __launch_bounds__(C::NT, C::OCC) void int4_tiled_kernel(Args p) {
     load_w(c[u % C::WS], u);
     fence();
   }
-  // The waves take the 32-row parts of the tile in turn: a tile with few rows is shared, and parts without any are
-  // not multiplied.
-  const int live = MODE == PLAIN ? TI : ((rows + 31) / 32 - wm + C::WM - 1) / C::WM;
   float unit[TJ];  // the sums are times this
 #pragma unroll
   for (int j = 0; j < TJ; ++j) unit[j] = 1.0f;
-  int xbuf = 0, xnext = C::XS - 1;
-  for (int t0 = 0; t0 < steps; t0 += C::WS) {
+  // The 32-row parts of a tile are dealt to its WM rows of waves in turn; of a tile with few rows only the first
+  // LIVE parts of each are multiplied (an expert's last tile: 3 of 8 of all rows of 256-row tiles at 222 pairs an
+  // expert), in code of their own, since branches around the instructions would keep them from overlapping.
+  auto multiply = [&](auto live) {
+    constexpr int LIVE = decltype(live)::value;
+    int xbuf = 0, xnext = C::XS - 1;
+    for (int t0 = 0; t0 < steps; t0 += C::WS) {
 #pragma unroll
-    for (int u = 0; u < C::WS; ++u) {
-      const int t = t0 + u;
-      if (t >= steps) break;
-      // X of this step has arrived, everybody's part of W is written, and the other buffers are read
-      __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
-      if (t < C::XS) wait_vmcnt<0>();      // the first loads were issued in another order
-      else wait_vmcnt<C::LATER>();
-      __builtin_amdgcn_s_barrier();
-      fence();
-      issue_x(t + C::XS - 1, xnext);
-      fence();
-      const uint8_t* xb = lds + xbuf * C::X_BYTES;
-      const uint8_t* wb = wlds + (t & 1) * C::W_BYTES;
-      bf16x8 a[2][TI], b[2][TJ];
-      auto read = [&](int kk) {
+      for (int u = 0; u < C::WS; ++u) {
+        const int t = t0 + u;
+        if (t >= steps) break;
+        // X of this step has arrived, everybody's part of W is written, and the other buffers are read
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+        if (t < C::XS) wait_vmcnt<0>();      // the first loads were issued in another order
+        else wait_vmcnt<C::LATER>();
+        __builtin_amdgcn_s_barrier();
+        fence();
+        issue_x(t + C::XS - 1, xnext);
+        fence();
+        const uint8_t* xb = lds + xbuf * C::X_BYTES;
+        const uint8_t* wb = wlds + (t & 1) * C::W_BYTES;
+        bf16x8 a[2][LIVE], b[2][TJ];
+        auto read = [&](int kk) {
 #pragma unroll
-        for (int i = 0; i < TI; ++i) {
-          if (i > 0 && i >= live) continue;  // uniform: no rows there
-          const int r = (i * C::WM + wm) * 32 + (lane & 31);
-          a[kk & 1][i] = __builtin_bit_cast(
-              bf16x8, *reinterpret_cast<const u32x4*>(xb + r * RB + 16 * swz16<P>(r, 2 * kk + (lane >> 5))));
-        }
+          for (int i = 0; i < LIVE; ++i) {
+            const int r = (i * C::WM + wm) * 32 + (lane & 31);
+            a[kk & 1][i] = __builtin_bit_cast(
+                bf16x8, *reinterpret_cast<const u32x4*>(xb + r * RB + 16 * swz16<P>(r, 2 * kk + (lane >> 5))));
+          }
 #pragma unroll
-        for (int j = 0; j < TJ; ++j) {
-          const int r = (wn * TJ + j) * 32 + (lane & 31);
-          b[kk & 1][j] = __builtin_bit_cast(
-              bf16x8, *reinterpret_cast<const u32x4*>(wb + r * RB + 16 * swz16<P>(r, 2 * kk + (lane >> 5))));
-        }
-      };
-      // at the first step of a group (groups of 32: twice a step)
-      auto rescale = [&](int h) {
+          for (int j = 0; j < TJ; ++j) {
+            const int r = (wn * TJ + j) * 32 + (lane & 31);
+            b[kk & 1][j] = __builtin_bit_cast(
+                bf16x8, *reinterpret_cast<const u32x4*>(wb + r * RB + 16 * swz16<P>(r, 2 * kk + (lane >> 5))));
+          }
+        };
+        // at the first step of a group (groups of 32: twice a step)
+        auto rescale = [&](int h) {
 #pragma unroll
-        for (int j = 0; j < TJ; ++j) {
-          const float m = mlds[((t & 1) * 2 + h) * C::BN + (wn * TJ + j) * 32 + (lane & 31)];
-          const float f = unit[j] / m;
-          unit[j] = m;
+          for (int j = 0; j < TJ; ++j) {
+            const float m = mlds[((t & 1) * 2 + h) * C::BN + (wn * TJ + j) * 32 + (lane & 31)];
+            const float f = unit[j] / m;
+            unit[j] = m;
 #pragma unroll
-          for (int i = 0; i < TI; ++i)
+            for (int i = 0; i < LIVE; ++i)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) acc[i][j][e] *= f;
-        }
-      };
-      read(0);
-      if (p.group != 128 || (t & 1) == 0) rescale(0);
+              for (int e = 0; e < 16; ++e) acc[i][j][e] *= f;
+          }
+        };
+        read(0);
+        if constexpr (G < 128) rescale(0);
+        else if (u % 2 == 0) rescale(0);
 #pragma unroll
-      for (int kk = 0; kk < KS / 16; ++kk) {
-        if (kk == 2 && p.group == 32) rescale(1);
-        if (kk + 1 < KS / 16) read(kk + 1);  // while this one is multiplied
+        for (int kk = 0; kk < KS / 16; ++kk) {
+          if (kk == 2 && G == 32) rescale(1);
+          if (kk + 1 < KS / 16) read(kk + 1);  // while this one is multiplied
 #pragma unroll
-        for (int i = 0; i < TI; ++i)
+          for (int i = 0; i < LIVE; ++i)
 #pragma unroll
-          for (int j = 0; j < TJ; ++j)
-            if (i == 0 || i < live)
+            for (int j = 0; j < TJ; ++j)
               acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[kk & 1][i], b[kk & 1][j], acc[i][j], 0, 0, 0);
-        store_w(c[(u + 1) % C::WS], t + 1, kk);  // past the last step: into a buffer that nobody reads
+          store_w(c[(u + 1) % C::WS], t + 1, kk);  // past the last step: into a buffer that nobody reads
+        }
+        load_w(c[(u + 1) % C::WS], t + 1 + C::WS);
+        fence();
+        xbuf = xbuf + 1 == C::XS ? 0 : xbuf + 1;
+        xnext = xnext + 1 == C::XS ? 0 : xnext + 1;
       }
-      load_w(c[(u + 1) % C::WS], t + 1 + C::WS);
-      fence();
-      xbuf = xbuf + 1 == C::XS ? 0 : xbuf + 1;
-      xnext = xnext + 1 == C::XS ? 0 : xnext + 1;
+    }
+  };
+  if constexpr (MODE == PLAIN) {
+    multiply(std::integral_constant<int, TI>());
+  } else {
+    const int live = (rows + 32 * C::WM - 1) / (32 * C::WM);  // uniform in the workgroup
+    if constexpr (TI == 4) {
+      if (live >= 4) multiply(std::integral_constant<int, 4>());
+      else if (live == 3) multiply(std::integral_constant<int, 3>());
+      else if (live == 2) multiply(std::integral_constant<int, 2>());
+      else multiply(std::integral_constant<int, 1>());
+    } else {
+      if (live >= 2) multiply(std::integral_constant<int, TI>());
+      else multiply(std::integral_constant<int, 1>());
     }
   }
   wait_vmcnt<0>();  // loads into LDS end before the workgroup does
@@ -280,7 +300,10 @@ hipError_t launch(Args a, int64_t tiles, hipStream_t s) {
   a.tiles = (int)tiles;
   const int64_t grid = (tiles * a.nblocks + 7) / 8 * 8;
   if (grid * C::NT >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;  // HIP counts threads in 32 bits
-  hipLaunchKernelGGL((int4_tiled_kernel<C, MODE>), dim3((uint32_t)grid), dim3(C::NT), 0, s, a);
+  const dim3 g((uint32_t)grid), block(C::NT);
+  if (a.group == 128) hipLaunchKernelGGL((int4_tiled_kernel<C, MODE, 128>), g, block, 0, s, a);
+  else if (a.group == 64) hipLaunchKernelGGL((int4_tiled_kernel<C, MODE, 64>), g, block, 0, s, a);
+  else hipLaunchKernelGGL((int4_tiled_kernel<C, MODE, 32>), g, block, 0, s, a);
   return hipGetLastError();
 }
 
@@ -288,9 +311,7 @@ template <int MODE, class F>
 hipError_t by_size(int cfg, Args a, F tiles, hipStream_t s) {
   switch (cfg) {
     case 0: return launch<TileCfg<256, 256, 2, 4, 2, 2, 2>, MODE>(a, tiles(256), s);
-    case 1: return launch<TileCfg<128, 256, 2, 4, 4, 3, 2>, MODE>(a, tiles(128), s);
     case 2: return launch<TileCfg<128, 128, 2, 2, 2, 2, 2>, MODE>(a, tiles(128), s);
-    case 3: return launch<TileCfg<64, 128, 2, 2, 4, 3, 2>, MODE>(a, tiles(64), s);
   }
   return hipErrorInvalidConfiguration;
 }

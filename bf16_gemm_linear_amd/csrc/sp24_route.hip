@@ -196,11 +196,10 @@ __global__ __launch_bounds__(256) void route_kernel(sp24_router r, Shape s, int6
     }
   } else {
     if (soft && !r.renormalise) {
-      // e^x for x far below 0 is inexact in proportion to x, and adds as little
-      float f = 0.0f;
+      sum = 0.0;
 #pragma unroll
-      for (int i = 0; i < V; ++i) f += __builtin_amdgcn_exp2f((l[i] - from) * 1.4426950408889634f);
-      sum = (double)wave_sum(f);
+      for (int i = 0; i < V; ++i) sum += l[i] == none ? 0.0 : exp_of((double)l[i] - from);
+      sum = wave_sum(sum);
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -266,8 +265,8 @@ __global__ __launch_bounds__(256) void route_kernel(sp24_router r, Shape s, int6
   if (soft) {
     // renormalised: relative to the largest that was chosen, so that none of them underflows
     const float big = r.renormalise ? wave_max(at) : from;
-    won = mine && at != none ? exp_of((double)at - (big == none ? 0.0f : big)) / (sum == 0.0 ? 1.0 : sum) : 0.0;
-    if (r.renormalise) won = mine && at != none ? exp_of((double)at - (big == none ? 0.0f : big)) : 0.0;
+    won = mine && at != none ? exp_of((double)at - (big == none ? 0.0f : big)) : 0.0;
+    if (!r.renormalise && sum != 0.0) won /= sum;
   } else {
     won = mine && at != none ? sigmoid((double)at) : 0.0;
   }
