@@ -82,7 +82,8 @@ hipError_t launch_int4_gemm(const Int4Gemm& a, float* part, hipStream_t s) {
 
 bool int4_experts_by_pairs(int64_t tokens, int64_t pairs, int64_t experts, int64_t d, int64_t f) {
   const int64_t used = pairs < experts ? pairs : experts;
-  return tokens <= 4 && (double)(pairs - used) * d * f * 1.5 <= 50e6;
+  const bool grids = pairs * f < (int64_t)1 << 25 && tokens * d < (int64_t)1 << 26;  // HIP counts threads in 32 bits
+  return tokens <= 4 && grids && (double)(pairs - used) * d * f * 1.5 <= 50e6;
 }
 
 // Pairs an expert, 64 experts of 4096 x 1792, 8 a token, gated and down in us:

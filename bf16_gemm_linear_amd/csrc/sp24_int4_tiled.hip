@@ -38,18 +38,16 @@ struct Args {
   int tiles, nblocks;  // row tiles (at most) and column tiles
 };
 
-// XS buffers of X in LDS (XS - 1 steps ahead), WS sets of W's codes in registers (WS steps ahead).
-template <int BM_, int BN_, int WM_, int WN_, int XS_, int WS_, int OCC_>
+// Two buffers of X and of W in LDS; W's codes are in registers two steps ahead.
+template <int BM_, int BN_, int WM_, int WN_>
 struct TileCfg {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, XS = XS_, WS = WS_, OCC = OCC_;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
   static constexpr int NT = WM * WN * 64, TI = BM / WM / 32, TJ = BN / WN / 32;
   static constexpr int X_I = BM / 8 / (WM * WN);  // load instructions of X a wave and step
-  static constexpr int X_BYTES = BM * RB, W_BYTES = BN * RB, M_OFF = XS * X_BYTES + 2 * W_BYTES;
-  static constexpr int LDS = M_OFF + 2 * 2 * BN * 4;  // and m of every row's two blocks of 32, two buffers
+  static constexpr int X_BYTES = BM * RB, W_BYTES = BN * RB, W_OFF = 2 * X_BYTES, M_OFF = W_OFF + 2 * W_BYTES;
+  static constexpr int ROW_OFF = M_OFF + 2 * 2 * BN * 4;  // behind m of every row's two blocks of 32, two buffers
+  static constexpr int LDS = ROW_OFF + BM * 4;            // and the pair of every row
   static_assert(X_I * 8 * WM * WN == BM && NT == BN * 2 && TI > 0 && TJ > 0 && LDS <= 160 * 1024, "tile");
-  // loads of a wave that can be outstanding while the X of a step has to be there: X of the steps behind it, and
-  // W's codes and scales (and zero points: then fewer are) issued since
-  static constexpr int LATER = (XS - 2) * X_I + (XS - 1) * 2;
 };
 
 // 8 codes -> 8 bf16 values (q - z) s; ns = -z s, s a power of two.
@@ -63,9 +61,8 @@ __device__ __forceinline__ u32x4 widen(uint32_t w, float s, float ns) {
 }
 
 template <class C, int MODE, int G>
-__global__ __launch_bounds__(C::NT, C::OCC) void int4_tiled_kernel(Args p) {
+__global__ __launch_bounds__(C::NT, 2) void int4_tiled_kernel(Args p) {
   constexpr int TI = C::TI, TJ = C::TJ, H = MODE == GATED ? 2 : 1;
-  static_assert(C::WS % 2 == 0, "a step's number and its copy's are even together");
   static_assert(MODE != GATED || TJ == 2, "a wave's gate tile and its up tile");
   __shared__ __attribute__((aligned(16))) uint8_t lds[C::LDS];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -89,65 +86,71 @@ __global__ __launch_bounds__(C::NT, C::OCC) void int4_tiled_kernel(Args p) {
   }
   const int n0 = nb * (C::BN / H);
 
-  // X: this lane's rows (of 8 an instruction), swizzled piece
-  const uint16_t* xrow[C::X_I];
-#pragma unroll
-  for (int j = 0; j < C::X_I; ++j) {
-    const int r = (wave * C::X_I + j) * 8 + lane / P;
-    size_t row = first + min(r, rows - 1);
-    if constexpr (MODE == GATED) row = p.pairs.order[row] / p.pairs.top;
-    xrow[j] = p.x + row * p.k;
-  }
-  // W: this thread has half `wh` (32 values of a step) of LDS row wr
-  const int groups = p.k / G;
-  constexpr int gshift = G == 32 ? 5 : G == 64 ? 6 : 7;
-  const int wh = tid & 1, wr = tid / 2;
-  size_t wrow;
-  {
-    int col = n0 + wr, half = 0;
-    if constexpr (MODE == GATED) {  // a wave's 64 rows: 32 gate rows, their up rows
-      col = n0 + wr / 64 * 32 + wr % 32;
-      half = wr / 32 % 2;
-    }
-    wrow = (size_t)expert * (H * p.n) + (size_t)half * p.n + min(col, p.n - 1);
-  }
-  const uint8_t* const wcode = p.w.codes + wrow * (p.k / 2);
-  const uint16_t* const wscale = p.w.scales + wrow * groups;
-  const uint8_t* const wzero = p.w.zeros == nullptr ? nullptr : p.w.zeros + wrow * groups;
+  int* const pair_of = reinterpret_cast<int*>(lds + C::ROW_OFF);  // DOWN: the pair of every row
+  if constexpr (MODE == DOWN)
+    for (int i = tid; i < rows; i += C::NT) pair_of[i] = p.pairs.order[first + i];
 
   const int steps = (p.k + KS - 1) / KS;
-  // Loads past the last step are that step's again, so that every step has the same number of them.
+  // Loads past the last step are that step's again, so that every step has the same number of them.  A last
+  // step of 32 values (groups of 32 alone) has its first half twice: the second meets values of W that are 0.
+  auto begin = [&](int t) { return min(t, steps - 1) * KS; };
+  auto half_step = [&](int k0) { return G == 32 && k0 + KS > p.k; };  // uniform
+  // X: this lane's rows (of 8 an instruction) and swizzled pieces, from uniform bases: PLAIN and DOWN 32-bit
+  // offsets (k <= 2^20, at most 256 rows)
+  const uint16_t* const x0 = MODE == GATED ? p.x : p.x + (size_t)first * p.k;
+  using Offset = std::conditional_t<MODE == GATED, size_t, uint32_t>;
+  Offset xoff[C::X_I];
+#pragma unroll
+  for (int j = 0; j < C::X_I; ++j) {
+    const int r = (wave * C::X_I + j) * 8 + lane / P, at = min(r, rows - 1);
+    Offset row = at;
+    if constexpr (MODE == GATED) row = p.pairs.order[first + at] / p.pairs.top;
+    xoff[j] = row * (Offset)p.k + 8 * swz16<P>(r, lane % P);
+  }
   auto issue_x = [&](int t, int buffer) {
-    const int k0 = min(t, steps - 1) * KS;
+    const int k0 = begin(t);
     uint8_t* buf = lds + buffer * C::X_BYTES;
 #pragma unroll
     for (int j = 0; j < C::X_I; ++j) {
-      const int i = wave * C::X_I + j, r = i * 8 + lane / P;
-      // past k: the row's last piece again, against values of W that are 0
-      const int at = min(k0 + 8 * swz16<P>(r, lane % P), p.k - 8);
-      dma16(xrow[j] + at, buf + i * 1024);
+      const int i = wave * C::X_I + j;
+      Offset o = xoff[j];
+      if (half_step(k0) && swz16<P>(i * 8 + lane / P, lane % P) >= P / 2) o -= KS / 2;
+      dma16(x0 + k0 + o, buf + i * 1024);
     }
   };
+  // W: this thread has half `wh` (32 values of a step) of LDS row wr.  A wave's 32 rows are neighbours (GATED: of
+  // every 64 rows the first 32 are gate rows, the others their up rows).
+  const int groups = p.k / G;
+  constexpr int gshift = G == 32 ? 5 : G == 64 ? 6 : 7;
+  const int wh = tid & 1, wr = tid / 2;
+  const int col0 = min(n0 + 32 * (MODE == GATED ? wave / 2 : wave), p.n - 1);
+  const uint32_t wlocal = (uint32_t)min(lane / 2, p.n - 1 - col0);
+  const size_t wrow = (size_t)expert * (H * p.n) + (MODE == GATED ? (size_t)(wave % 2) * p.n : 0) + col0;
+  const uint8_t* const wcode = p.w.codes + wrow * (p.k / 2);
+  const uint16_t* const wscale = p.w.scales + wrow * groups;
+  const uint8_t* const wzero = p.w.zeros == nullptr ? nullptr : p.w.zeros + wrow * groups;
+  const uint32_t coff = wlocal * (uint32_t)(p.k / 2) + 16 * wh, soff = wlocal * (uint32_t)groups + (G == 32 ? wh : 0);
   struct Codes {
     u32x4 q;
     uint32_t s, z;
   };
   auto load_w = [&](Codes& c, int t) {
-    const int k = min(t * KS + 32 * wh, p.k - 32);
-    c.q = *reinterpret_cast<const u32x4*>(wcode + k / 2);
-    c.s = wscale[k >> gshift];
-    c.z = p.w.zeros == nullptr ? kInt4Zero : wzero[k >> gshift];
+    const int k0 = begin(t);
+    const uint32_t back = half_step(k0) ? wh : 0;
+    c.q = *reinterpret_cast<const u32x4*>(wcode + k0 / 2 + (coff - 16 * back));
+    c.s = (wscale + (k0 >> gshift))[soff - back];
+    c.z = p.w.zeros == nullptr ? kInt4Zero : (wzero + (k0 >> gshift))[soff - back];
   };
-  uint8_t* const wlds = lds + C::XS * C::X_BYTES;
+  uint8_t* const wlds = lds + C::W_OFF;
   float* const mlds = reinterpret_cast<float*>(lds + C::M_OFF);
-  // values 8 d .. 8 d + 7 of the thread's 32 of step t
-  auto store_w = [&](const Codes& c, int t, int d) {
+  // values 8 d .. 8 d + 7 of the thread's 32 of step t, into buffer b
+  auto store_w = [&](const Codes& c, int t, int b, int d) {
     // 2^e: the exponent's bits alone (2^-126 for subnormals, whose m is below 1; Inf and NaN: Inf).  Past k and
     // with a scale of 0: values 0 whatever the codes, and m = 1.
     const bool none = t * KS + 32 * wh >= p.k || (c.s & 0x7FFFu) == 0;
     const uint32_t exponent = (c.s & 0x7F80u) << 16;
     const float s = none ? 0.0f : __uint_as_float(max(exponent, 0x00800000u));
-    *reinterpret_cast<u32x4*>(wlds + (t & 1) * C::W_BYTES + wr * RB + 16 * swz16<P>(wr, 4 * wh + d)) =
+    *reinterpret_cast<u32x4*>(wlds + b * C::W_BYTES + wr * RB + 16 * swz16<P>(wr, 4 * wh + d)) =
         widen(c.q[d], s, -(float)c.z * s);
     if (d == 0) {
       // the mantissa and the sign, in 1's binade; a subnormal's without the leading bit; NaN stays one
@@ -155,7 +158,7 @@ __global__ __launch_bounds__(C::NT, C::OCC) void int4_tiled_kernel(Args p) {
       float m = __uint_as_float(one);
       if (exponent == 0) m -= __uint_as_float((c.s & 0x8000u) << 16 | 0x3F800000u);
       if (exponent == 0x7F800000u) m = (c.s & 0x7Fu) != 0 ? __builtin_nanf("") : __uint_as_float(one & 0xFF800000u);
-      mlds[((t & 1) * 2 + wh) * C::BN + wr] = none ? 1.0f : m;
+      mlds[(b * 2 + wh) * C::BN + wr] = none ? 1.0f : m;
     }
   };
 
@@ -171,20 +174,17 @@ __global__ __launch_bounds__(C::NT, C::OCC) void int4_tiled_kernel(Args p) {
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
   };
-  Codes c[C::WS];
+  Codes c[2];
   issue_x(0, 0);
   fence();
   load_w(c[0], 0);
 #pragma unroll
-  for (int u = 1; u < C::XS - 1; ++u) issue_x(u, u);
+  for (int d = 0; d < 4; ++d) store_w(c[0], 0, 0, d);
   fence();
-#pragma unroll
-  for (int d = 0; d < 4; ++d) store_w(c[0], 0, d);
-#pragma unroll
-  for (int u = 1; u <= C::WS; ++u) {
-    load_w(c[u % C::WS], u);
-    fence();
-  }
+  load_w(c[1], 1);
+  fence();
+  load_w(c[0], 2);
+  fence();
   float unit[TJ];  // the sums are times this
 #pragma unroll
   for (int j = 0; j < TJ; ++j) unit[j] = 1.0f;
@@ -193,22 +193,21 @@ __global__ __launch_bounds__(C::NT, C::OCC) void int4_tiled_kernel(Args p) {
   // expert), in code of their own, since branches around the instructions would keep them from overlapping.
   auto multiply = [&](auto live) {
     constexpr int LIVE = decltype(live)::value;
-    int xbuf = 0, xnext = C::XS - 1;
-    for (int t0 = 0; t0 < steps; t0 += C::WS) {
+    for (int t0 = 0; t0 < steps; t0 += 2) {
 #pragma unroll
-      for (int u = 0; u < C::WS; ++u) {
+      for (int u = 0; u < 2; ++u) {  // the buffers' number too
         const int t = t0 + u;
         if (t >= steps) break;
         // X of this step has arrived, everybody's part of W is written, and the other buffers are read
         __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
-        if (t < C::XS) wait_vmcnt<0>();      // the first loads were issued in another order
-        else wait_vmcnt<C::LATER>();
+        if (t < 2) wait_vmcnt<0>();  // the first loads were issued in another order
+        else wait_vmcnt<2>();        // those of W behind it are two, or three with zero points
         __builtin_amdgcn_s_barrier();
         fence();
-        issue_x(t + C::XS - 1, xnext);
+        issue_x(t + 1, 1 - u);
         fence();
-        const uint8_t* xb = lds + xbuf * C::X_BYTES;
-        const uint8_t* wb = wlds + (t & 1) * C::W_BYTES;
+        const uint8_t* xb = lds + u * C::X_BYTES;
+        const uint8_t* wb = wlds + u * C::W_BYTES;
         bf16x8 a[2][LIVE], b[2][TJ];
         auto read = [&](int kk) {
 #pragma unroll
@@ -228,7 +227,7 @@ __global__ __launch_bounds__(C::NT, C::OCC) void int4_tiled_kernel(Args p) {
         auto rescale = [&](int h) {
 #pragma unroll
           for (int j = 0; j < TJ; ++j) {
-            const float m = mlds[((t & 1) * 2 + h) * C::BN + (wn * TJ + j) * 32 + (lane & 31)];
+            const float m = mlds[(u * 2 + h) * C::BN + (wn * TJ + j) * 32 + (lane & 31)];
             const float f = unit[j] / m;
             unit[j] = m;
 #pragma unroll
@@ -249,15 +248,15 @@ __global__ __launch_bounds__(C::NT, C::OCC) void int4_tiled_kernel(Args p) {
 #pragma unroll
             for (int j = 0; j < TJ; ++j)
               acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[kk & 1][i], b[kk & 1][j], acc[i][j], 0, 0, 0);
-          store_w(c[(u + 1) % C::WS], t + 1, kk);  // past the last step: into a buffer that nobody reads
+          store_w(c[1 - u], t + 1, 1 - u, kk);  // past the last step: into a buffer that nobody reads
         }
-        load_w(c[(u + 1) % C::WS], t + 1 + C::WS);
+        load_w(c[1 - u], t + 3);
         fence();
-        xbuf = xbuf + 1 == C::XS ? 0 : xbuf + 1;
-        xnext = xnext + 1 == C::XS ? 0 : xnext + 1;
       }
     }
   };
+  // Half of a SIMD's two waves ahead of the other: left alone they multiply and widen at the same times.
+  if (C::NT == 512 && wm == 1) __builtin_amdgcn_s_setprio(1);
   if constexpr (MODE == PLAIN) {
     multiply(std::integral_constant<int, TI>());
   } else {
@@ -286,7 +285,7 @@ __global__ __launch_bounds__(C::NT, C::OCC) void int4_tiled_kernel(Args p) {
         if (row >= rows) continue;
         float v = acc[i][j][e] * unit[j];
         if constexpr (MODE == GATED) v = silu_mul(v, acc[i][TJ - 1][e] * unit[TJ - 1]);
-        if constexpr (MODE == DOWN) p.part[(size_t)p.pairs.order[first + row] * p.n + col] = v;
+        if constexpr (MODE == DOWN) p.part[(size_t)pair_of[row] * p.n + col] = v;
         else p.y[(size_t)(first + row) * p.n + col] = (uint16_t)f32x2_to_bf16x2(v, 0.0f);
       }
     }
@@ -310,8 +309,8 @@ hipError_t launch(Args a, int64_t tiles, hipStream_t s) {
 template <int MODE, class F>
 hipError_t by_size(int cfg, Args a, F tiles, hipStream_t s) {
   switch (cfg) {
-    case 0: return launch<TileCfg<256, 256, 2, 4, 2, 2, 2>, MODE>(a, tiles(256), s);
-    case 2: return launch<TileCfg<128, 128, 2, 2, 2, 2, 2>, MODE>(a, tiles(128), s);
+    case 0: return launch<TileCfg<256, 256, 2, 4>, MODE>(a, tiles(256), s);
+    case 2: return launch<TileCfg<128, 128, 2, 2>, MODE>(a, tiles(128), s);
   }
   return hipErrorInvalidConfiguration;
 }
