@@ -80,7 +80,7 @@ struct Int4Experts {
 };
 hipError_t launch_int4_experts(const Int4Experts& a, hipStream_t s);
 // Few tokens: a pair at a time (launch_int4_vec_experts), each streaming its expert's weights, unless more than
-// about 50 MB of them would be read again: what ordering the pairs costs, in bytes.
+// 25 MB of them would be read again, which takes as long as ordering the pairs and joining their outputs.
 bool int4_experts_by_pairs(int64_t tokens, int64_t pairs, int64_t experts, int64_t d, int64_t f);
 
 // The kernels.  sp24_int4_vec.hip: a few tokens; the experts' block with pairs in their own order, y being

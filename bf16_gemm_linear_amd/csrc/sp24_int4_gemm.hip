@@ -83,38 +83,69 @@ hipError_t launch_int4_gemm(const Int4Gemm& a, float* part, hipStream_t s) {
 bool int4_experts_by_pairs(int64_t tokens, int64_t pairs, int64_t experts, int64_t d, int64_t f) {
   const int64_t used = pairs < experts ? pairs : experts;
   const bool grids = pairs * f < (int64_t)1 << 25 && tokens * d < (int64_t)1 << 26;  // HIP counts threads in 32 bits
-  return tokens <= 4 && grids && (double)(pairs - used) * d * f * 1.5 <= 50e6;
+  return tokens <= 64 && grids && (double)(pairs - used) * d * f * 1.5 <= 25e6;
 }
 
-// Pairs an expert, 64 experts of 4096 x 1792, 8 a token, gated and down in us:
-//              slab, tiles of 16   slab, tiles of 32   128 x 128 tiles   256 x 256 tiles
-//   8 (64)        126 + 69            161 + 82            394 + 202
-//   16 (128)      182 + 95            186 + 106           397 + 208
-//   37 (300)      -                   329 + 167           289 + 167         352 + 198
-//   75 (600)      -                   571 + 279           349 + 210         376 + 221
-//   150 (1200)    -                   1049 + 498          532 + 332         467 + 312
-//   222 (1777)    -                   1515 + 691          718 + 445         619 + 407
-hipError_t launch_int4_experts(const Int4Experts& a, hipStream_t s) {
-  const int64_t each = a.pairs.count / a.pairs.experts;  // pairs of an expert
-  if (each <= 28) {
-    SlabPlan q;
-    q.mb = each <= 12 ? 1 : 2;
-    const int fits = 2048 / q.mb;  // 64 KB of X: two workgroups a CU
-    q.cbs = 4;
-    q.kp = 2;
-    q.slice = a.d;
-    q.chunk = a.d < fits ? a.d : fits;
-    const hipError_t e = launch_int4_slab_gated(q, a, s);
-    if (e != hipSuccess) return e;
-    q.cbs = 8;
-    q.kp = 1;
-    q.slice = a.f;
-    q.chunk = a.f < fits ? a.f : fits;
-    return launch_int4_slab_down(q, a, s);
+// An expert product's kernel, by its expected time: `rows` rows of W an expert (gated: gate and up rows), k values.
+// Half of each expert's last tile is taken to be empty.  Measured for 64 experts of 4096 x 1792, 8 a token, gated
+// and down in us:
+//   pairs an expert   slab, tiles of 16   slab, tiles of 32   128 x 128 tiles   256 x 256 tiles
+//   8                   126 + 69            161 + 82            394 + 202
+//   16                  182 + 95            186 + 106           397 + 208
+//   37                  -                   329 + 167           289 + 167         352 + 198
+//   75                  -                   571 + 279           349 + 210         376 + 221
+//   150                 -                   1049 + 498          532 + 332         467 + 312
+//   222                 -                   1515 + 691          671 + 379         600 + 350
+struct ExpertsPlan {
+  int slab, tiled;  // tokens / 16 of a slab workgroup, or 0 and a tiled configuration
+};
+ExpertsPlan experts_plan(const Pairs& p, int64_t rows, int64_t k, int group) {
+  const double pairs = (double)p.count, used = pairs < p.experts ? pairs : p.experts;
+  auto tiles = [&](int bm) {
+    const double t = pairs / bm + 0.5 * used;
+    return t > used ? t : used;
+  };
+  const double hbm = used * rows * k / 2 / 5e6;
+  double least = 1e30;
+  ExpertsPlan best{1, 0};
+  for (int mb = 1; mb <= 2; ++mb) {
+    const double wg = tiles(16 * mb) * up(rows, 64), few = wg < kCus ? kCus / wg : 1;
+    const double compute = tiles(16 * mb) * up(rows, 32) * up(k, 128) / kCus * (mb == 1 ? 0.13 : 0.2) * few;
+    const double t = 3 + (compute > hbm ? compute : hbm);
+    if (t < least) {
+      least = t;
+      best = ExpertsPlan{mb, 0};
+    }
   }
-  const int cfg = each <= 110 ? 2 : 0;
-  const hipError_t e = launch_int4_tiled_gated(cfg, a, s);
-  return e != hipSuccess ? e : launch_int4_tiled_down(cfg, a, s);
+  const double slower = group == 128 ? 1 : group == 64 ? 1.1 : 1.27;  // the sums' rescaling
+  const double small = tiles(128) * up(rows, 128), large = tiles(256) * up(rows, 256), steps = (double)up(k, 64) * slower;
+  const double t2 = 4 + (small <= kCus ? 1.0 : 1.4 * (small < 2 * kCus ? 1 : small / (2 * kCus))) * steps;
+  const double t0 = 4 + 1.95 * (large < kCus ? 1 : large / kCus) * steps;
+  if (t2 < least) {
+    least = t2;
+    best = ExpertsPlan{0, 2};
+  }
+  if (t0 < least) best = ExpertsPlan{0, 0};
+  return best;
+}
+
+// A slab workgroup of 8 waves: as many columns as leave every CU a workgroup; 64 KB of X, so that two fit a CU.
+SlabPlan experts_slab(const ExpertsPlan& e, const Pairs& p, int64_t rows, int64_t k, int most) {
+  const int64_t tiles = p.count < p.experts ? p.count : p.experts;
+  int cbs = most;
+  while (cbs > 2 && tiles * up(rows, 32 * cbs) < kCus) cbs /= 2;
+  const int fits = 2048 / e.slab;
+  return SlabPlan{e.slab, cbs, 8 / cbs, (int)k, (int)(k < fits ? k : fits)};
+}
+
+hipError_t launch_int4_experts(const Int4Experts& a, hipStream_t s) {
+  const ExpertsPlan g = experts_plan(a.pairs, 2 * (int64_t)a.f, a.d, a.group);
+  hipError_t e = g.slab ? launch_int4_slab_gated(experts_slab(g, a.pairs, 2 * (int64_t)a.f, a.d, 4), a, s)
+                        : launch_int4_tiled_gated(g.tiled, a, s);
+  if (e != hipSuccess) return e;
+  const ExpertsPlan d = experts_plan(a.pairs, a.d, a.f, a.group);
+  return d.slab ? launch_int4_slab_down(experts_slab(d, a.pairs, a.d, a.f, 8), a, s)
+                : launch_int4_tiled_down(d.tiled, a, s);
 }
 
 }  // namespace sp24
