@@ -19,16 +19,10 @@ __global__ __launch_bounds__(kSortThreads) void sort_pairs_kernel(const int32_t*
   const int run = (count + kSortThreads - 1) / kSortThreads * 64;
   const int from = wave * run, to = min(count, from + run);
   int below = 0, mine = 0;
-#pragma unroll 4
-  for (int i = from + lane; i < to; i += 64) {
-    const int id = ids[i];
-    below += id >= 0 && id < e;
-    mine += id == e;
-  }
-#pragma unroll
-  for (int o = 1; o < 64; o *= 2) {
-    below += __shfl_xor(below, o);
-    mine += __shfl_xor(mine, o);
+  for (int i0 = from; i0 < to; i0 += 64) {
+    const int i = i0 + lane, id = i < to ? ids[i] : -1;
+    mine += __popcll(__ballot(id == e));
+    below += __popcll(__ballot(id >= 0 && id < e));
   }
   if (lane == 0) {
     sums[wave][0] = mine;
@@ -60,14 +54,24 @@ __global__ __launch_bounds__(256) void join_pairs_kernel(const float* __restrict
                                                          const int32_t* __restrict__ ids,
                                                          const float* __restrict__ weights, int64_t units, int quads,
                                                          int top, int experts, uint16_t* __restrict__ y) {
+  constexpr int J = 8;  // slots whose loads are in flight together
   for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < units; u += (int64_t)gridDim.x * 256) {
     const int64_t t = u / quads;
     const int q = (int)(u - t * quads);
     f32x4 sum{0.f, 0.f, 0.f, 0.f};
-    for (int j = 0; j < top; ++j) {
-      const int64_t p = t * top + j;
-      if ((uint32_t)ids[p] >= (uint32_t)experts) continue;
-      sum += weights[p] * reinterpret_cast<const f32x4*>(part)[p * quads + q];
+    for (int j0 = 0; j0 < top; j0 += J) {
+      f32x4 v[J];
+      float w[J];
+#pragma unroll
+      for (int i = 0; i < J; ++i) {
+        const int64_t p = t * top + min(j0 + i, top - 1);
+        const bool there = j0 + i < top && (uint32_t)ids[p] < (uint32_t)experts;
+        v[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        w[i] = there ? weights[p] : 0.0f;
+        if (there) v[i] = reinterpret_cast<const f32x4*>(part)[p * quads + q];
+      }
+#pragma unroll
+      for (int i = 0; i < J; ++i) sum += w[i] * v[i];
     }
     reinterpret_cast<u32x2*>(y)[u] = u32x2{f32x2_to_bf16x2(sum[0], sum[1]), f32x2_to_bf16x2(sum[2], sum[3])};
   }

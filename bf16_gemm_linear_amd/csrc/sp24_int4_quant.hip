@@ -35,6 +35,15 @@ __device__ __forceinline__ uint32_t scale_bits(float s) {
   return b == 0 ? 0x3F80u : b;
 }
 
+// a / b from r, about 1 / b: one correction with the exact remainder.  What fp32 holds comes out exactly (a tie
+// between two codes, say), the rest to its last bit, which does not matter (see above).
+__device__ __forceinline__ float quotient(float a, float b, float r) {
+  const float q = a * r;
+  return fmaf(fmaf(-q, b, a), r, q);
+}
+// Where neither leaves fp32's normal range.
+__device__ __forceinline__ bool plain(float v) { return v > 0x1p-50f && v < 0x1p50f; }
+
 // units of 8 values; units < 2^31 * 32
 template <int GROUP, bool ZEROS>
 __global__ __launch_bounds__(kThreads) void int4_quant_kernel(const uint16_t* __restrict__ w, int64_t units,
@@ -66,23 +75,22 @@ __global__ __launch_bounds__(kThreads) void int4_quant_kernel(const uint16_t* __
       hi = __uint_as_float(group_fold<LANES>(__float_as_uint(hi), f_max));
       neg = __uint_as_float(group_fold<LANES>(__float_as_uint(-lo), f_max));  // -lo >= 0
       const float range = hi + neg;  // beyond fp32 for the largest values: their halves are not
-      sb = scale_bits(range < __builtin_inff() ? range / 15.0f : (0.5f * hi + 0.5f * neg) / 7.5f);
+      if (plain(range)) sb = scale_bits(quotient(range, 15.0f, 1.0f / 15.0f));
+      else sb = scale_bits(range < __builtin_inff() ? range / 15.0f : (0.5f * hi + 0.5f * neg) / 7.5f);
     } else {
-      sb = scale_bits(__uint_as_float(key << 16) / 7.0f);
+      const float amax = __uint_as_float(key << 16);
+      sb = scale_bits(plain(amax) ? quotient(amax, 7.0f, 1.0f / 7.0f) : amax / 7.0f);
     }
     const float s = __uint_as_float(sb << 16);
-    if constexpr (ZEROS) z = fminf(rintf(neg / s), 15.0f);
     float t[8];
-    if (s > 0x1p-60f && s < 0x1p60f) {
-      // w r and one correction with the exact remainder: what is a tie comes out exactly, and the rest
-      // lies too far from one for the last bit to matter
-      const float r = 1.0f / s;
+    if (plain(s)) {
+      float r = __builtin_amdgcn_rcpf(s);  // to an ulp or two
+      r = fmaf(fmaf(-r, s, 1.0f), r, r);
+      if constexpr (ZEROS) z = fminf(rintf(quotient(neg, s, r)), 15.0f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float a = v[i] * r;
-        t[i] = fmaf(fmaf(-a, s, v[i]), r, a);
-      }
-    } else {  // r or the remainder can leave fp32's range
+      for (int i = 0; i < 8; ++i) t[i] = quotient(v[i], s, r);
+    } else {  // the reciprocal or the remainder can leave fp32's range
+      if constexpr (ZEROS) z = fminf(rintf(neg / s), 15.0f);
 #pragma unroll
       for (int i = 0; i < 8; ++i) t[i] = v[i] / s;
     }

@@ -21,6 +21,15 @@ namespace {
 
 constexpr float kMaxLogit = 3.402823466e38f;  // +inf counts as this
 
+// The unsigned numbers whose order is that of a double's upper word or of a float (no NaN: the least; no -0).
+__device__ __forceinline__ uint32_t order_key(uint32_t bits, bool number) {
+  return number ? bits ^ ((uint32_t)((int32_t)bits >> 31) | 0x80000000u) : 0u;
+}
+__device__ __forceinline__ uint32_t order_key(float v) { return order_key(__float_as_uint(v), v == v); }
+__device__ __forceinline__ uint32_t order_key(double v) {
+  return order_key((uint32_t)(__builtin_bit_cast(uint64_t, v) >> 32), v == v);
+}
+
 // The value of the lane OFF away (for 4 and 8 one of the aligned group of OFF lanes there).
 template <int OFF, class T>
 __device__ __forceinline__ void pair_of(T v, T& a, T& b) {
@@ -192,7 +201,7 @@ __global__ __launch_bounds__(256) void route_kernel(sp24_router r, Shape s, int6
         second = larger(second, best < v ? best : v);
         best = larger(best, v);
       }
-      if (i >= held) c[i] = gone;
+      c[i] = i < held ? c[i] + 0.0 : gone;  // no -0
     }
   } else {
     if (soft && !r.renormalise) {
@@ -205,7 +214,7 @@ __global__ __launch_bounds__(256) void route_kernel(sp24_router r, Shape s, int6
     for (int i = 0; i < V; ++i) {
       c[i] = l[i] > none ? l[i] : none;
       best = larger(best, c[i]);
-      if (i >= held) c[i] = gone;
+      c[i] = i < held ? c[i] + 0.0f : gone;  // no -0
     }
   }
 
@@ -242,12 +251,19 @@ __global__ __launch_bounds__(256) void route_kernel(sp24_router r, Shape s, int6
     T v = c[0];
 #pragma unroll
     for (int i = 1; i < V; ++i) v = larger(v, c[i]);
-    v = wave_max(v);
-    int at = V;  // the first of this lane's with that value
+    int at = 0;  // the first of this lane's with that value
 #pragma unroll
     for (int i = V - 1; i >= 0; --i)
       if (c[i] == v) at = i;
-    const int winner = __ffsll((unsigned long long)__ballot(at < V)) - 1;
+    // 32 bits of each lane's best are compared; all of them only where those are equal
+    const uint32_t key = order_key(v);
+    uint32_t most_key = fold_wave(key, bits_max);
+    uint64_t first = __ballot(key == most_key);
+    if (WIDE && (first & (first - 1)) != 0) {
+      const T all = wave_max(key == most_key ? v : gone);
+      first = __ballot(v == all);
+    }
+    const int winner = __ffsll((unsigned long long)first) - 1;
     const int e = __builtin_amdgcn_readlane(e0 + at, winner);
 #pragma unroll
     for (int i = 0; i < V; ++i)
