@@ -2,7 +2,7 @@
 //
 // Slab kernel, in microseconds, with W = the workgroups, `steps` = 32 columns x 128 values of a row tile a CU:
 //   3 + max(steps t, HBM) + (X + W through L2) / 26 TB/s + 2.2 + slices (0.3 + a slice's sums through memory),
-// t = 0.09 for tiles of 16 tokens and 0.14 for 32, steps in whole rounds of W over 256 CUs.
+// t = 0.1 for tiles of 16 tokens and 0.14 for 32, steps in whole rounds of W over 256 CUs.
 // Tiled kernel: 4 + rounds * steps of 64 values * t, t by tile.  Measured beside it (HIP graphs):
 //   16 x 4096 x 14336 13.7 (expected 13.7), 16 x 14336 x 4096 11.5 (11.2), 128 x 4096 x 14336 40 (45).
 #include "sp24_int4.hpp"
@@ -34,7 +34,7 @@ double slab_plan(int64_t m, int64_t n, int64_t k, SlabPlan& best) {
         const int64_t slice = slices == 1 ? k : up(up(k, slices), 128) * 128;
         const double rounds = (double)up(wg, kCus) * kCus / wg;
         const double steps = (double)tiles * up(n, 32) * up(k, 128) / kCus * rounds;
-        const double compute = steps * (mb == 1 ? 0.09 : 0.14), hbm = (double)n * k / 2 / 5e6;
+        const double compute = steps * (mb == 1 ? 0.1 : 0.14), hbm = (double)n * k / 2 / 5e6;
         double t = 3 + (compute > hbm ? compute : hbm) + ((double)across * m * k * 2 + (double)tiles * n * k / 2) / 26e6;
         if (slices > 1) t += 2.2 + slices * (0.3 + (double)m * n * 8 / 8e6);
         if (t < least) {

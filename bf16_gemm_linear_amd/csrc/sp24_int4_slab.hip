@@ -13,9 +13,9 @@
 // 32; accumulator register e is token 4 (l / 16) + e, W row l % 16.  A lane loads 16 bytes of codes, block
 // l / 16 of its row's four; a transposition of the 4 x 4 words of lanes l, l + 16, l + 32, l + 48 (four
 // register exchanges) gives it word l / 16 of every block, so each instruction covers one block of 32 and
-// any group size works.  Codes become the bf16 pairs (128 + q); what that adds, 128 + z times the sum of
-// x, is taken off in fp32 behind a group's sum, the sum of x coming from one more instruction
-// with ones.  Rows past the last are the last one again; their outputs are not stored.
+// any group size works.  Codes become the bf16 pairs (128 + q); what that adds is taken off again: without zero
+// points the sums start from those of -136 x, one more instruction for all the workgroup's columns, and with
+// them (128 + z) times the sum of x, from an instruction with ones, in fp32 behind a group's sum.  Rows past the last are the last one again; their outputs are not stored.
 #include "sp24_dma.hpp"
 #include "sp24_int4.hpp"
 #include "sp24_mx4.hpp"
@@ -51,8 +51,8 @@ __device__ __forceinline__ void transpose4(uint32_t (&v)[4]) {
 
 constexpr int F = 4;  // scales that a thread loads at a time
 
-// G128: a scale covers a whole step; otherwise it is applied every 32 values.
-template <int RB, int MB, int S, int MODE, bool G128>
+// G128: a scale covers a whole step; otherwise it is applied every 32 values.  Z: with zero points.
+template <int RB, int MB, int S, int MODE, bool G128, bool Z>
 __global__ __launch_bounds__(1024, 4) void int4_slab_kernel(Args p) {
   constexpr int H = MODE == GATED ? 2 : 1, OB = RB / H;  // gate rows and up rows; row blocks of the output
   static_assert(OB > 0, "GATED needs a gate and an up block");
@@ -97,7 +97,8 @@ __global__ __launch_bounds__(1024, 4) void int4_slab_kernel(Args p) {
     for (int j = 0; j < MB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   const f32x4 zero{0.f, 0.f, 0.f, 0.f};
   const Int4Bits bits;
-  const bf16x8 ones = __builtin_bit_cast(bf16x8, u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
+  constexpr uint32_t all = Z ? 0x3F803F80u : 0xC308C308u;  // pairs of 1, or of -136
+  const bf16x8 constant = __builtin_bit_cast(bf16x8, u32x4{all, all, all, all});
 
   for (int k0 = kbegin; k0 < kend; k0 += p.chunk) {
     const int kc = min(p.chunk, kend - k0);               // values of this pass
@@ -139,39 +140,54 @@ __global__ __launch_bounds__(1024, 4) void int4_slab_kernel(Args p) {
           // past the row's end (a last step of fewer than four blocks): unused
           const uint32_t s = both(i, G128 ? 0 : min(d >> gshift, gc - 1 - (4 * step >> gshift)));
           sc[i][d] = __uint_as_float(s & 0xFFFF0000u);
-          zp[i][d] = 128.0f + (float)(s & 255u);
+          zp[i][d] = Z ? 128.0f + (float)(s & 255u) : 0.0f;
         }
       }
       const int left = blocks - 4 * step;  // G128: at least four
 #pragma unroll
       for (int j = 0; j < MB; ++j) {
+        // a group's sums of this row block's columns, of x times the constant `sx`
+        auto add = [&](int i, int d, const f32x4& v, const f32x4& sx) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][j][e] += sc[i][d] * (Z ? v[e] - zp[i][d] * sx[e] : v[e]);
+        };
         if constexpr (G128) {
+          // 16 tokens: the step's X stays in registers, and the columns' sums start from sx; for 32 there is no room
+          constexpr bool KEEP = MB == 1;
+          bf16x8 a[KEEP ? 4 : 1];
           f32x4 v[RB], sx = zero;
 #pragma unroll
           for (int i = 0; i < RB; ++i) v[i] = zero;
+          auto columns = [&](int d, const bf16x8& x) {
+#pragma unroll
+            for (int i = 0; i < RB; ++i) v[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, b[i][d], v[i], 0, 0, 0);
+          };
 #pragma unroll
           for (int d = 0; d < 4; ++d) {
-            const bf16x8 a = x(j, d);
-            sx = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, ones, sx, 0, 0, 0);
+            a[KEEP ? d : 0] = x(j, d);
+            sx = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[KEEP ? d : 0], constant, sx, 0, 0, 0);
+            if constexpr (!KEEP) columns(d, a[0]);
+          }
+          if constexpr (KEEP) {
 #pragma unroll
-            for (int i = 0; i < RB; ++i) v[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b[i][d], v[i], 0, 0, 0);
+            for (int i = 0; i < RB; ++i) v[i] = Z ? zero : sx;
+#pragma unroll
+            for (int d = 0; d < 4; ++d) columns(d, a[d]);
+          } else if constexpr (!Z) {
+#pragma unroll
+            for (int i = 0; i < RB; ++i) v[i] += sx;
           }
 #pragma unroll
-          for (int i = 0; i < RB; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[i][j][e] += sc[i][0] * (v[i][e] - zp[i][0] * sx[e]);
+          for (int i = 0; i < RB; ++i) add(i, 0, v[i], sx);
         } else {
 #pragma unroll
           for (int d = 0; d < 4; ++d) {
             if (d >= left) break;  // uniform
             const bf16x8 a = x(j, d);
-            const f32x4 sx = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, ones, zero, 0, 0, 0);
+            const f32x4 sx = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, constant, zero, 0, 0, 0);
 #pragma unroll
-            for (int i = 0; i < RB; ++i) {
-              const f32x4 v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b[i][d], zero, 0, 0, 0);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) acc[i][j][e] += sc[i][d] * (v[e] - zp[i][d] * sx[e]);
-            }
+            for (int i = 0; i < RB; ++i)
+              add(i, d, __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b[i][d], Z ? zero : sx, 0, 0, 0), sx);
           }
         }
       }
@@ -205,7 +221,7 @@ __global__ __launch_bounds__(1024, 4) void int4_slab_kernel(Args p) {
           const bool up = H == 2 && at >= cols;
           const uint32_t o = (uint32_t)min(up ? at - cols : at, ncols - 1) * (uint32_t)groups + (uint32_t)(g0 + g);
           fs[f] = (up ? scales_up : scales)[o];
-          fz[f] = zeros == nullptr ? kInt4Zero : (up ? zeros_up : zeros)[o];
+          fz[f] = Z ? (up ? zeros_up : zeros)[o] : 0;
         }
 #pragma unroll
         for (int f = 0; f < F; ++f)
@@ -308,10 +324,12 @@ hipError_t launch(Args a, const SlabPlan& q, int64_t tiles, hipStream_t s) {
   if (lds > kLds || waves < 1 || waves > 16) return hipErrorInvalidConfiguration;
   const int64_t grid = tiles * ((a.n + cols - 1) / cols);
   if (grid * waves * 64 >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;  // HIP counts threads in 32 bits
-  if (a.group == 128)
-    hipLaunchKernelGGL((int4_slab_kernel<RB, MB, S, MODE, true>), dim3((uint32_t)grid), dim3(waves * 64), lds, s, a);
-  else
-    hipLaunchKernelGGL((int4_slab_kernel<RB, MB, S, MODE, false>), dim3((uint32_t)grid), dim3(waves * 64), lds, s, a);
+  const dim3 g((uint32_t)grid), block(waves * 64);
+  const bool z = a.w.zeros != nullptr;
+  if (a.group == 128 && z) hipLaunchKernelGGL((int4_slab_kernel<RB, MB, S, MODE, true, true>), g, block, lds, s, a);
+  else if (a.group == 128) hipLaunchKernelGGL((int4_slab_kernel<RB, MB, S, MODE, true, false>), g, block, lds, s, a);
+  else if (z) hipLaunchKernelGGL((int4_slab_kernel<RB, MB, S, MODE, false, true>), g, block, lds, s, a);
+  else hipLaunchKernelGGL((int4_slab_kernel<RB, MB, S, MODE, false, false>), g, block, lds, s, a);
   return hipGetLastError();
 }
 

@@ -57,8 +57,18 @@ __device__ __forceinline__ void pair_of(T v, T& a, T& b) {
     }
   }
 }
-__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }  // not the NaN
-__device__ __forceinline__ double larger(double a, double b) { return fmax(a, b); }
+// The larger, of a number and a NaN the number.  The instructions by name: the compiler's fmax first makes every
+// operand a quiet NaN in an instruction of its own, which all NaN here are.
+__device__ __forceinline__ float larger(float a, float b) {
+  float r;
+  asm("v_max_f32 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+  return r;
+}
+__device__ __forceinline__ double larger(double a, double b) {
+  double r;
+  asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+  return r;
+}
 
 template <int OFF, class T>
 __device__ __forceinline__ T step_max(T v) {
@@ -91,32 +101,34 @@ __device__ __forceinline__ void step_two(T& best, T& second) {
 }
 
 // e^x to about 2^-51, x <= 0 (below -745: 0; NaN stays one): x = k ln 2 + r, the series of e^r to its
-// fourteenth term (|r| <= 0.347: the next is below 2^-57).
+// fourteenth term (|r| <= 0.347: the next is below 2^-57).  All V together: the coefficients are loaded once.
+template <int V>
+__device__ __forceinline__ void exps_of(double (&x)[V]) {
+  constexpr double coefficient[] = {1.0 / 479001600.0, 1.0 / 39916800.0, 1.0 / 3628800.0, 1.0 / 362880.0, 1.0 / 40320.0,
+                                    1.0 / 5040.0,      1.0 / 720.0,      1.0 / 120.0,     1.0 / 24.0,     1.0 / 6.0,
+                                    0.5,               1.0,              1.0};
+  double k[V], r[V], p[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    k[i] = rint(x[i] * 1.4426950408889634);
+    r[i] = fma(k[i], -0.6931471824645996, x[i]);  // ln 2 as the nearest float (k times it is exact) and the rest
+    r[i] = fma(k[i], 1.90465429995776805e-09, r[i]);
+    p[i] = 1.0 / 6227020800.0;
+  }
+#pragma unroll
+  for (int c = 0; c < 13; ++c)
+#pragma unroll
+    for (int i = 0; i < V; ++i) p[i] = fma(p[i], r[i], coefficient[c]);
+#pragma unroll
+  for (int i = 0; i < V; ++i) x[i] = x[i] < -745.0 ? 0.0 : __builtin_amdgcn_ldexp(p[i], (int)fmax(k[i], -2000.0));
+}
 __device__ __forceinline__ double exp_of(double x) {
-  const double k = rint(x * 1.4426950408889634);
-  double r = fma(k, -6.93147182464599609e-01, x);  // ln 2 as the nearest float (k times it is exact) and the rest
-  r = fma(k, 1.90465429995776805e-09, r);
-  double p = 1.0 / 6227020800.0;
-  p = fma(p, r, 1.0 / 479001600.0);
-  p = fma(p, r, 1.0 / 39916800.0);
-  p = fma(p, r, 1.0 / 3628800.0);
-  p = fma(p, r, 1.0 / 362880.0);
-  p = fma(p, r, 1.0 / 40320.0);
-  p = fma(p, r, 1.0 / 5040.0);
-  p = fma(p, r, 1.0 / 720.0);
-  p = fma(p, r, 1.0 / 120.0);
-  p = fma(p, r, 1.0 / 24.0);
-  p = fma(p, r, 1.0 / 6.0);
-  p = fma(p, r, 0.5);
-  p = fma(p, r, 1.0);
-  p = fma(p, r, 1.0);
-  return x < -745.0 ? 0.0 : __builtin_amdgcn_ldexp(p, (int)fmax(k, -2000.0));
+  double v[1] = {x};
+  exps_of(v);
+  return v[0];
 }
-// sigmoid, from e^-|x|
-__device__ __forceinline__ double sigmoid(double x) {
-  const double e = exp_of(-fabs(x));
-  return (x < 0.0 ? e : 1.0) / (1.0 + e);
-}
+// sigmoid of x, e being e^-|x|
+__device__ __forceinline__ double sigmoid(double x, double e) { return (x < 0.0 ? e : 1.0) / (1.0 + e); }
 
 struct Shape {
   int experts, top, groups, per, lanes_log2;  // per: experts of a group; 2^lanes_log2 lanes hold it
@@ -169,8 +181,8 @@ __global__ __launch_bounds__(256) void route_kernel(sp24_router r, Shape s, int6
   float most = none;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    l[i] = l[i] > kMaxLogit ? kMaxLogit : l[i];
-    most = fmaxf(most, l[i]);  // passes over a NaN
+    l[i] = l[i] != l[i] ? __builtin_nanf("") : l[i] > kMaxLogit ? kMaxLogit : l[i];  // every NaN a quiet one
+    most = larger(most, l[i]);  // passes over a NaN
   }
   if (soft) most = wave_max(most);
   // a row without numbers has no e^(l - most); its scores are 0 (or NaN)
@@ -181,7 +193,8 @@ __global__ __launch_bounds__(256) void route_kernel(sp24_router r, Shape s, int6
   T best = none, second = none;
   if constexpr (WIDE) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) c[i] = l[i] == none ? 0.0 : soft ? exp_of((double)l[i] - from) : sigmoid((double)l[i]);
+    for (int i = 0; i < V; ++i) c[i] = l[i] == none ? -1000.0 : soft ? (double)l[i] - from : -fabs((double)l[i]);
+    exps_of(c);  // 0 for -1000
     if (soft) {
       sum = 0.0;
 #pragma unroll
@@ -189,6 +202,9 @@ __global__ __launch_bounds__(256) void route_kernel(sp24_router r, Shape s, int6
       sum = wave_sum(sum);
 #pragma unroll
       for (int i = 0; i < V; ++i) c[i] = sum == 0.0 ? 0.0 : c[i] / sum;
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) c[i] = sigmoid((double)l[i], c[i]);  // of -inf: 0
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -205,9 +221,13 @@ __global__ __launch_bounds__(256) void route_kernel(sp24_router r, Shape s, int6
     }
   } else {
     if (soft && !r.renormalise) {
+      double x[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[i] = l[i] == none ? -1000.0 : (double)l[i] - from;
+      exps_of(x);
       sum = 0.0;
 #pragma unroll
-      for (int i = 0; i < V; ++i) sum += l[i] == none ? 0.0 : exp_of((double)l[i] - from);
+      for (int i = 0; i < V; ++i) sum += x[i];
       sum = wave_sum(sum);
     }
 #pragma unroll
@@ -260,6 +280,7 @@ __global__ __launch_bounds__(256) void route_kernel(sp24_router r, Shape s, int6
     uint32_t most_key = fold_wave(key, bits_max);
     uint64_t first = __ballot(key == most_key);
     if (WIDE && (first & (first - 1)) != 0) {
+      asm volatile("");  // a branch, not both sides
       const T all = wave_max(key == most_key ? v : gone);
       first = __ballot(v == all);
     }
@@ -277,14 +298,14 @@ __global__ __launch_bounds__(256) void route_kernel(sp24_router r, Shape s, int6
   if (mine)
     at = BF16 ? bf16_to_f32(static_cast<const uint16_t*>(logits)[row + id])
               : static_cast<const float*>(logits)[row + id];
-  at = at > kMaxLogit ? kMaxLogit : at;
+  at = at != at ? __builtin_nanf("") : at > kMaxLogit ? kMaxLogit : at;
   if (soft) {
     // renormalised: relative to the largest that was chosen, so that none of them underflows
     const float big = r.renormalise ? wave_max(at) : from;
     won = mine && at != none ? exp_of((double)at - (big == none ? 0.0f : big)) : 0.0;
     if (!r.renormalise && sum != 0.0) won /= sum;
   } else {
-    won = mine && at != none ? sigmoid((double)at) : 0.0;
+    won = mine && at != none ? sigmoid((double)at, exp_of(-fabs((double)at))) : 0.0;
   }
   if (r.renormalise) {
     const double all = wave_sum(won);

@@ -113,6 +113,21 @@ def test_nan_keeps_ids_valid(e, kind):
                 assert 7 not in got[2] and set(got[4][:3]) == {e - 3, e - 2, e - 1}
 
 
+@pytest.mark.parametrize("bits", [0x7F81, 0xFF81, 0x7FC1, 0x7FFF])
+def test_every_kind_of_nan(bits):
+    """Signalling ones too: maxima that meet them go on to the numbers."""
+    sp = need_sp()
+    announce("route nan bits", hex(bits))
+    for e in (16, 60, 256):
+        l = torch.randn(9, e, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16)
+        l.view(torch.int16)[:, 3::5] = bits - 0x10000 if bits >= 0x8000 else bits
+        want, _ = R.route(l.double().numpy(), 4)
+        for x in (l, l.float()):
+            for b in (None, torch.zeros(e, device=DEV)):
+                ids, _ = sp.route(x.to(DEV), 4, kind=sp.ROUTE_SIGMOID, bias=b)
+                assert np.array_equal(ids.cpu().numpy(), want)
+
+
 def test_near_scores():
     """Scores that differ by less than fp32 holds, with a bias: the order is that of 64 bits."""
     announce("route near scores")
