@@ -83,7 +83,7 @@ hipError_t launch_int4_experts(const Int4Experts& a, hipStream_t s);
 // 25 MB of them would be read again, which takes as long as ordering the pairs and joining their outputs.
 bool int4_experts_by_pairs(int64_t tokens, int64_t pairs, int64_t experts, int64_t d, int64_t f);
 
-// The kernels.  sp24_int4_vec.hip: a few tokens; the experts' block with pairs in their own order, y being
+// The kernels.  sp24_int4_vec.hip: one or two tokens; the experts' block with pairs in their own order, y being
 // its output.
 hipError_t launch_int4_vec(const Int4Gemm& g, hipStream_t s);
 hipError_t launch_int4_vec_experts(const Int4Experts& e, const int32_t* ids, const float* weights, uint16_t* y,
@@ -98,7 +98,7 @@ struct SlabPlan {
 hipError_t launch_int4_slab(const SlabPlan& q, const Int4Gemm& g, float* part, hipStream_t s);
 hipError_t launch_int4_slab_gated(const SlabPlan& q, const Int4Experts& e, hipStream_t s);
 hipError_t launch_int4_slab_down(const SlabPlan& q, const Int4Experts& e, hipStream_t s);
-// sp24_int4_tiled.hip: configuration cfg.
+// sp24_int4_tiled.hip: tiles of 256 x 256 (cfg 0) or 128 x 128 (cfg 1).
 hipError_t launch_int4_tiled(int cfg, const Int4Gemm& g, hipStream_t s);
 hipError_t launch_int4_tiled_gated(int cfg, const Int4Experts& e, hipStream_t s);
 hipError_t launch_int4_tiled_down(int cfg, const Int4Experts& e, hipStream_t s);

@@ -52,7 +52,7 @@ double tiled_plan(int64_t m, int64_t n, int64_t k, int& cfg) {
   const int64_t large = up(m, 256) * up(n, 256), small = up(m, 128) * up(n, 128);
   const double t0 = 4 + up(large, kCus) * steps * 2.0;
   const double t2 = 4 + (small <= kCus ? 1.0 : up(small, 2 * kCus) * 1.47) * steps;
-  cfg = t0 < t2 ? 0 : 2;
+  cfg = t0 < t2 ? 0 : 1;
   return t0 < t2 ? t0 : t2;
 }
 
@@ -123,7 +123,7 @@ ExpertsPlan experts_plan(const Pairs& p, int64_t rows, int64_t k, int group) {
   const double t0 = 4 + 1.95 * (large < kCus ? 1 : large / kCus) * steps;
   if (t2 < least) {
     least = t2;
-    best = ExpertsPlan{0, 2};
+    best = ExpertsPlan{0, 1};
   }
   if (t0 < least) best = ExpertsPlan{0, 0};
   return best;

@@ -310,7 +310,7 @@ template <int MODE, class F>
 hipError_t by_size(int cfg, Args a, F tiles, hipStream_t s) {
   switch (cfg) {
     case 0: return launch<TileCfg<256, 256, 2, 4>, MODE>(a, tiles(256), s);
-    case 2: return launch<TileCfg<128, 128, 2, 2>, MODE>(a, tiles(128), s);
+    case 1: return launch<TileCfg<128, 128, 2, 2>, MODE>(a, tiles(128), s);
   }
   return hipErrorInvalidConfiguration;
 }

@@ -1,6 +1,7 @@
-// Products with integer 4-bit weights for one to four tokens: the weight's bytes are the time.
+// Products with integer 4-bit weights for one or two tokens, and the experts' block for a few, pair by
+// pair: the weight's bytes are the time.
 //
-// A workgroup holds RB rows of W, a wave of it a chunk of 2048 values of K, lane l of it the 32 values of block l: each
+// A workgroup holds 8 rows of W, a wave of it a chunk of 2048 values of K, lane l of it the 32 values of block l: each
 // row's load is 1 KB of neighbouring bytes, and the lane's x stays in registers for all rows.  No LDS
 // before the end, no waits between waves: what is in flight at once is a decode step's whole share of
 // W (n = 14336, k = 4096: 14 waves a CU of 8 KB each).
@@ -9,6 +10,8 @@
 // s (sum x (128 + q) - (128 + z) sum x), in fp32; a block of 32 lies in one group.
 // The lanes' sums are joined by register exchanges (rows and lanes transposed on the way), those of
 // the chunks through LDS, in a fixed order.
+//
+// MEASURED_VEC
 #include "sp24_int4.hpp"
 #include "sp24_mx4.hpp"
 
@@ -18,7 +21,7 @@ namespace {
 enum { PLAIN = 0, GATED = 1, DOWN = 2 };
 
 struct Args {
-  int m, n, k, group;  // n: output columns (GATED: W has 2 n rows an expert)
+  int n, k, group;  // n: output columns (GATED: W has 2 n rows an expert)
   const uint16_t* x;
   Int4Weight w;
   uint16_t* y;
@@ -50,15 +53,17 @@ __device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float c) {
   return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, a), __builtin_bit_cast(bf16x2, b), c, false);
 }
 
-// RB rows a workgroup (GATED: half of them gate rows, half their up rows); MT tokens.
-template <int MT, int RB, int MODE, int OCC>
+constexpr int RB = 8;  // rows of W a workgroup (GATED: half of them gate rows, half their up rows)
+
+// MT tokens.
+template <int MT, int MODE, int OCC>
 __global__ __launch_bounds__(512, OCC) void int4_vec_kernel(Args p) {
   constexpr int OUT = MODE == GATED ? RB / 2 : RB;  // outputs a workgroup
   __shared__ float red[8][RB * MT];
   const int tid = threadIdx.x, lane = tid & 63;
   const int kw = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int nblocks = (p.n + OUT - 1) / OUT;
-  const int64_t item = blockIdx.x / nblocks;  // PLAIN: tokens from MT item; GATED: a pair; DOWN: a token
+  const int64_t item = blockIdx.x / nblocks;  // PLAIN: 0; GATED: a pair; DOWN: a token
   const int n0 = (int)(blockIdx.x % nblocks) * OUT;
   const int blocks = p.k / 32, chunks = (blocks + 63) / 64, groups = p.k / p.group;
   const int gshift = p.group == 32 ? 0 : p.group == 64 ? 1 : 2;
@@ -110,7 +115,7 @@ __global__ __launch_bounds__(512, OCC) void int4_vec_kernel(Args p) {
     float sx[MT];
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
-      const size_t tok = MODE == PLAIN ? min(item * MT + t, (int64_t)p.m - 1) : 0;
+      const size_t tok = MODE == PLAIN ? t : 0;
       const u32x4* xp = reinterpret_cast<const u32x4*>(xr + tok * p.k + (size_t)kb * 32);
       sx[t] = 0.0f;
 #pragma unroll
@@ -148,18 +153,10 @@ __global__ __launch_bounds__(512, OCC) void int4_vec_kernel(Args p) {
     float v[RB / 2];
 #pragma unroll
     for (int r = 0; r < RB / 2; ++r) v[r] = merge<32>(acc[2 * r][t], acc[2 * r + 1][t], lane);
-    float u = merge<16>(v[0], v[1], lane);
-    int row = (lane >> 5 & 1) | (lane >> 4 & 1) << 1;
-    uint32_t f;
-    if constexpr (RB == 8) {
-      u = merge<8>(u, merge<16>(v[2], v[3], lane), lane);
-      row |= (lane >> 3 & 1) << 2;
-      f = __float_as_uint(u);
-      f = fold_lanes<4>(fold_lanes<2>(fold_lanes<1>(f, bits_sum), bits_sum), bits_sum);
-    } else {
-      f = __float_as_uint(u);
-      f = fold_lanes<8>(fold_lanes<4>(fold_lanes<2>(fold_lanes<1>(f, bits_sum), bits_sum), bits_sum), bits_sum);
-    }
+    const float u = merge<8>(merge<16>(v[0], v[1], lane), merge<16>(v[2], v[3], lane), lane);
+    const int row = (lane >> 5 & 1) | (lane >> 4 & 1) << 1 | (lane >> 3 & 1) << 2;
+    const uint32_t f =
+        fold_lanes<4>(fold_lanes<2>(fold_lanes<1>(__float_as_uint(u), bits_sum), bits_sum), bits_sum);
     if ((lane & (64 / RB - 1)) == 0) red[kw][row * MT + t] = __uint_as_float(f);
   }
   __syncthreads();
@@ -171,39 +168,37 @@ __global__ __launch_bounds__(512, OCC) void int4_vec_kernel(Args p) {
       if constexpr (MODE == GATED) u += red[z][(i + OUT) * MT + t];
     }
     if constexpr (MODE == GATED) v = silu_mul(v, u);
-    const int64_t row = MODE == PLAIN ? item * MT + t : item;
-    if (n0 + i < p.n && (MODE != PLAIN || row < p.m))
+    const int64_t row = MODE == PLAIN ? t : item;
+    if (n0 + i < p.n)
       p.y[(size_t)row * p.n + n0 + i] = (uint16_t)f32x2_to_bf16x2(v, 0.0f);
   }
 }
 
-template <int MT, int RB, int MODE, int OCC>
+template <int MT, int MODE, int OCC>
 hipError_t launch(Args a, int64_t items, hipStream_t s) {
   constexpr int OUT = MODE == GATED ? RB / 2 : RB;
   const int work = (a.k / 32 + 63) / 64 * (MODE == DOWN ? a.top : 1);
   a.kw = work < 8 ? work : 8;
   const int64_t grid = items * ((a.n + OUT - 1) / OUT);
   if (grid * 64 * a.kw >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;  // HIP counts threads in 32 bits
-  hipLaunchKernelGGL((int4_vec_kernel<MT, RB, MODE, OCC>), dim3((uint32_t)grid), dim3(64 * a.kw), 0, s, a);
+  hipLaunchKernelGGL((int4_vec_kernel<MT, MODE, OCC>), dim3((uint32_t)grid), dim3(64 * a.kw), 0, s, a);
   return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_int4_vec(const Int4Gemm& g, hipStream_t s) {
-  const Args a{g.m, g.n, g.k, g.group, g.x, g.w, g.y, nullptr, nullptr, 1, 1, 0};
-  if (g.m == 1) return launch<1, 8, PLAIN, 5>(a, 1, s);
-  if (g.m == 2) return launch<2, 8, PLAIN, 4>(a, 1, s);
-  return launch<4, 4, PLAIN, 4>(a, (g.m + 3) / 4, s);
+  const Args a{g.n, g.k, g.group, g.x, g.w, g.y, nullptr, nullptr, 1, 1, 0};
+  return g.m == 1 ? launch<1, PLAIN, 5>(a, 1, s) : launch<2, PLAIN, 4>(a, 1, s);
 }
 
 hipError_t launch_int4_vec_experts(const Int4Experts& e, const int32_t* ids, const float* weights, uint16_t* y,
                                    hipStream_t s) {
-  const Args gated{0, e.f, e.d, e.group, e.x, e.gu, e.h, ids, weights, e.pairs.experts, e.pairs.top, 0};
-  const hipError_t st = launch<1, 8, GATED, 5>(gated, e.pairs.count, s);
+  const Args gated{e.f, e.d, e.group, e.x, e.gu, e.h, ids, weights, e.pairs.experts, e.pairs.top, 0};
+  const hipError_t st = launch<1, GATED, 5>(gated, e.pairs.count, s);
   if (st != hipSuccess) return st;
-  const Args down{0, e.d, e.f, e.group, e.h, e.down, y, ids, weights, e.pairs.experts, e.pairs.top, 0};
-  return launch<1, 8, DOWN, 4>(down, e.tokens, s);
+  const Args down{e.d, e.f, e.group, e.h, e.down, y, ids, weights, e.pairs.experts, e.pairs.top, 0};
+  return launch<1, DOWN, 4>(down, e.tokens, s);
 }
 
 }  // namespace sp24

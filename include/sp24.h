@@ -654,7 +654,8 @@ typedef struct sp24_int4_experts {
  * Requires 1 <= experts <= 1024, 1 <= top <= 64, tokens >= 1, tokens * top <= 2^21,
  * group <= d, f <= 2^20, d % group == f % group == 0.
  *   ws/ws_bytes: sp24_experts_int4_workspace_size(tokens, d, f, experts, top).  No host
- * synchronisation. */
+ * synchronisation.  (SP24_ERR_HIP where no grid covers the outputs; one does while
+ * (tokens * top / 16 + min(tokens * top, experts)) * max(d, f) is at most 2^28.) */
 int sp24_experts_int4(const sp24_int4_experts* w, int64_t tokens, int64_t top, const void* x_bf16, const int32_t* ids,
                       const float* weights_f32, void* y_bf16, void* ws, size_t ws_bytes, void* stream);
 
