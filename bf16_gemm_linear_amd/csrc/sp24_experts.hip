@@ -7,6 +7,7 @@ namespace sp24 {
 namespace {
 
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
+constexpr int kSortLoads = 4;  // of a lane's ids in flight
 
 // Workgroup e finds the places of expert e: it counts the ids below e (where its range begins) and lists
 // the pairs with id e, in their order, without atomics: a wave takes a run of neighbouring pairs, 64 at a
@@ -18,11 +19,22 @@ __global__ __launch_bounds__(kSortThreads) void sort_pairs_kernel(const int32_t*
   const int e = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int run = (count + kSortThreads - 1) / kSortThreads * 64;
   const int from = wave * run, to = min(count, from + run);
+  auto load = [&](int i0, int (&id)[kSortLoads]) {
+#pragma unroll
+    for (int j = 0; j < kSortLoads; ++j) {
+      const int i = i0 + 64 * j + lane;
+      id[j] = i < to ? ids[i] : -1;
+    }
+  };
   int below = 0, mine = 0;
-  for (int i0 = from; i0 < to; i0 += 64) {
-    const int i = i0 + lane, id = i < to ? ids[i] : -1;
-    mine += __popcll(__ballot(id == e));
-    below += __popcll(__ballot(id >= 0 && id < e));
+  for (int i0 = from; i0 < to; i0 += 64 * kSortLoads) {
+    int id[kSortLoads];
+    load(i0, id);
+#pragma unroll
+    for (int j = 0; j < kSortLoads; ++j) {
+      mine += __popcll(__ballot(id[j] == e));
+      below += __popcll(__ballot(id[j] >= 0 && id[j] < e));
+    }
   }
   if (lane == 0) {
     sums[wave][0] = mine;
@@ -41,11 +53,15 @@ __global__ __launch_bounds__(kSortThreads) void sort_pairs_kernel(const int32_t*
     if (e == experts - 1) offsets[experts] = start + all;
   }
   int at = start + before;
-  for (int i0 = from; i0 < to; i0 += 64) {
-    const int i = i0 + lane;
-    const uint64_t here = __ballot(i < to && ids[min(i, count - 1)] == e);
-    if (here >> lane & 1) order[at + __popcll(here & (((uint64_t)1 << lane) - 1))] = i;
-    at += __popcll(here);
+  for (int i0 = from; i0 < to; i0 += 64 * kSortLoads) {
+    int id[kSortLoads];
+    load(i0, id);
+#pragma unroll
+    for (int j = 0; j < kSortLoads; ++j) {
+      const uint64_t here = __ballot(id[j] == e);
+      if (here >> lane & 1) order[at + __popcll(here & (((uint64_t)1 << lane) - 1))] = i0 + 64 * j + lane;
+      at += __popcll(here);
+    }
   }
 }
 

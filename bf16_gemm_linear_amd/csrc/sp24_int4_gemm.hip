@@ -74,6 +74,10 @@ hipError_t launch_int4_gemm(const Int4Gemm& a, float* part, hipStream_t s) {
     if (slab_plan(a.m, a.n, a.k, q) <= tiled) {
       const int fits = slab_chunk(a.m < 16 * q.mb ? a.m : 16 * q.mb, 32 * q.cbs, a.group);
       q.chunk = q.slice < fits ? q.slice : fits;
+      // Several passes over LDS: three waves a SIMD instead of two hide more of their starts.  With two and three,
+      // us: 77 x 6144 x 4096 by groups of 32 22.0 and 20.2, 96 x 6144 x 4096 by 64 25.6 and 22.5; in one pass by
+      // 128 48 x 14336 x 4096 30.2 and 31.1, 16 x 28672 x 4096 18.5 and 19.5.
+      if (q.cbs == 4 && q.chunk < q.slice) q.kp = 3;
       return launch_int4_slab(q, a, part, s);
     }
   }
