@@ -4,7 +4,9 @@
 //   3 + max(steps t, HBM) + (X + W through L2) / 26 TB/s + 2.2 + slices (0.3 + a slice's sums through memory),
 // t = 0.1 for tiles of 16 tokens and 0.14 for 32, steps in whole rounds of W over 256 CUs.
 // Tiled kernel: 4 + rounds * steps of 64 values * t, t by tile.  Measured beside it (HIP graphs):
-//   16 x 4096 x 14336 13.7 (expected 13.7), 16 x 14336 x 4096 11.5 (11.2), 128 x 4096 x 14336 40 (45).
+// us and in parentheses expected, eight weights in turn: 16 x 4096 x 14336 15.6 (14.8), 16 x 14336 x 4096 13.4 (11.7),
+// 32 17.6 (15.3), 64 x 4096 x 14336 27 (28), 128 40 (47); tiled: 256 x 14336 x 4096 58 (68), 2047 x 28672 x 8192 994
+// (1028), where the slab kernel would take 88 and 2400.
 #include "sp24_int4.hpp"
 
 namespace sp24 {

@@ -7,7 +7,9 @@
 // bf16 values that is not a tie lies further than 2^-17 of it from one, so quotients to fp32 that are exact where
 // fp32 holds them give the codes of exact arithmetic.
 //
-// A lane takes 8 values (a 16-byte load, a 4-byte store), group / 8 lanes a group.
+// A lane takes 8 values (a 16-byte load, a 4-byte store), group / 8 lanes a group: one pass, the group's extremes by
+// register exchanges.  HBM bounds both ways: 28672 x 8192 by 64 with zero points (598 MB) 124 to 142 us, back 114 to
+// 120 (5.0 to 5.2 TB/s; a copy 5.17); 4096 x 14336 by 128 26 and 29.
 #include "sp24_fp8.hpp"
 #include "sp24_int4.hpp"
 #include "sp24_mx4.hpp"

@@ -15,7 +15,14 @@
 // register exchanges) gives it word l / 16 of every block, so each instruction covers one block of 32 and
 // any group size works.  Codes become the bf16 pairs (128 + q); what that adds is taken off again: without zero
 // points the sums start from those of -136 x, one more instruction for all the workgroup's columns, and with
-// them (128 + z) times the sum of x, from an instruction with ones, in fp32 behind a group's sum.  Rows past the last are the last one again; their outputs are not stored.
+// them (128 + z) times the sum of x, from an instruction with ones, in fp32 behind a group's sum.  Rows past the last
+// are the last one again; their outputs are not stored.
+//
+// 16 x 4096 x 14336 with zero points takes 12.4 to 13.4 us and 2.8 to 3.9 for the join (14.1 a call), 16 x 14336 x
+// 4096 11.6; what is left over the weight's 6 is X, a launch and its end.  77 x 6144 x 4096 by groups of 32
+// takes 20.3, of which about 12 are the vector instructions that widen W for each of five row tiles and scale a
+// sum every 32 values.  Tiles of 48 tokens and more widen less and spill.  64 experts of 4096 x 1792 at 29 tokens:
+// 112 to 117 us gated (492 MB: 4.2 to 4.4 TB/s), 65 to 68 down.
 #include "sp24_dma.hpp"
 #include "sp24_int4.hpp"
 #include "sp24_mx4.hpp"

@@ -13,6 +13,9 @@
 // once, and the lowest lane that holds a value has the lowest index.  An expert that was taken, or is in no chosen
 // group, is NaN, which maxima pass over.  Reductions are register exchanges (sp24_mx4.hpp's).  The weights are
 // formed by the first `top` lanes, each from its expert's logit, in 64 bits.
+//
+// One token takes 2.6 us, a launch and a trip to memory; 8191 tokens x 256 experts in 8 groups with a bias, 8 taken,
+// 15.3: some 1000 instructions a token, not its 1 KB, which alone would take 1.7.  4000 x 60, 4 taken: 4.6.
 #include "sp24_int4.hpp"
 #include "sp24_mx4.hpp"
 

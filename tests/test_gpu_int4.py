@@ -5,7 +5,9 @@ two are exact in fp32 in any order, so they must be the bf16 rounding of the exa
 |y - ref| <= 2^-8 |ref| + 2^-17 A + (k / 32 + 16) 2^-24 B.  The first term is half a bf16 step.  A = sum of |x|
 (128 + max(q, z)) |s|, twice over: a kernel may form x (128 + q) and x (128 + z) apart; a group's sum has at most
 128 / 32 + 32 roundings or truncations of 2^-23, below 2^-17.8.  B = sum |x w|, joined over at most k / 32 groups
-and 16 waves in fp32."""
+and 16 waves in fp32.  Where a kernel multiplies (q - z) and rescales its sums a group at a time, it rounds them
+3 k / 32 times (an instruction every 16 values, a quotient and a product a group) by 2^-24 of at most B, and
+A >= 8 B."""
 import numpy as np
 import pytest
 import torch
