@@ -35,7 +35,8 @@ __all__ = [
     "prune_compress", "decompress", "quant_fp8", "gemm", "dense_gemm", "workspace_size", "plan",
     "quant_mxfp4", "dequant_mxfp4", "gemm_mxfp4", "gated_mxfp4", "rmsnorm", "ffn_mxfp4", "ffn_mxfp4_workspace_size",
     "mxfp4_scale_index", "NORM_BF16", "NORM_FP8_ROWS", "NORM_INT8_ROWS", "NORM_FP8_GROUPS", "NORM_MXFP4",
-    "quant_int4", "dequant_int4", "gemm_int4", "gemm_int4_workspace_size", "pack_int4", "unpack_int4", "route", "ROUTE_SOFTMAX", "ROUTE_SIGMOID",
+    "quant_int4", "dequant_int4", "gemm_int4", "gemm_int4_workspace_size", "pack_int4", "unpack_int4", "route",
+    "ROUTE_SOFTMAX", "ROUTE_SIGMOID",
     "experts_int4", "experts_int4_workspace_size",
     "probe_mfma_layout", "probe_mfma_rate", "probe_copy", "probe_read", "probe_ring",
 ]

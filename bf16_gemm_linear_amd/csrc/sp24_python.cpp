@@ -1,6 +1,6 @@
-// CPython binding of the MXFP4 and integer 4-bit operators, the norm, the router and the experts:
-// the checks of the tensors, their allocation and the call in one step, since a decode step's kernels (3 to 8 us) are shorter
-// than the same checks written in Python (rmsnorm 7.7 us a call through ctypes).
+// CPython binding of the MXFP4 and integer 4-bit operators, the norm, the router and the experts: the
+// checks of the tensors, their allocation and the call in one step, since a decode step's kernels
+// (3 to 8 us) are shorter than the same checks written in Python (rmsnorm 7.7 us a call through ctypes).
 //
 // The package exports these functions as they are (a Python function around each adds 0.1 to
 // 0.2 us).  None stands for an absent tensor.  Errors are TypeError and ValueError for
@@ -595,7 +595,8 @@ bool intern(Function& f) {
   return true;
 }
 bool prepare() {
-  for (Function* f : {&g_quant, &g_dequant, &g_gemm, &g_gated, &g_rmsnorm, &g_ffn, &g_quant4, &g_dequant4, &g_gemm4, &g_route, &g_experts})
+  for (Function* f : {&g_quant, &g_dequant, &g_gemm, &g_gated, &g_rmsnorm, &g_ffn, &g_quant4, &g_dequant4, &g_gemm4,
+                      &g_route, &g_experts})
     if (!intern(*f)) return false;
   PyObject* const eps = PyFloat_FromDouble(1e-6);
   g_gated.defaults[4] = Py_False;
