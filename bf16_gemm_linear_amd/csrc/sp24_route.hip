@@ -15,7 +15,8 @@
 // formed by the first `top` lanes, each from its expert's logit, in 64 bits.
 //
 // One token takes 2.6 us, a launch and a trip to memory; 8191 tokens x 256 experts in 8 groups with a bias, 8 taken,
-// 15.3: some 1000 instructions a token, not its 1 KB, which alone would take 1.7.  4000 x 60, 4 taken: 4.6.
+// 14.5 a call: some 850 vector instructions a token, 30 of them a pick, not its 1 KB, which alone would take 1.7.
+// 4000 x 60, 4 taken: 4.1 a call.
 #include "sp24_int4.hpp"
 #include "sp24_mx4.hpp"
 
@@ -270,29 +271,88 @@ __global__ __launch_bounds__(256) void route_kernel(sp24_router r, Shape s, int6
 
   // slot j's expert ends in lane j (top <= 64)
   int id = 0;
-  for (int j = 0; j < s.top; ++j) {
-    T v = c[0];
+  if constexpr (V <= 4) {
+    // Few values a lane: sorted once, the best first and of equal ones the lower index, so that a pick looks at
+    // every lane's first alone and the winner's move up (8191 x 256, 32 taken: 23.4 us from 28.5; 8 taken 13.9 from
+    // 14.6).  As 32-bit words in their order: a double's upper one and, for those equal, its lower one.  Sorting
+    // more than four would take longer than the picks.
+    int e[V];
+    uint32_t key[V], low[V];
 #pragma unroll
-    for (int i = 1; i < V; ++i) v = larger(v, c[i]);
-    int at = 0;  // the first of this lane's with that value
+    for (int i = 0; i < V; ++i) e[i] = e0 + i;
 #pragma unroll
-    for (int i = V - 1; i >= 0; --i)
-      if (c[i] == v) at = i;
-    // 32 bits of each lane's best are compared; all of them only where those are equal
-    const uint32_t key = order_key(v);
-    uint32_t most_key = fold_wave(key, bits_max);
-    uint64_t first = __ballot(key == most_key);
-    if (WIDE && (first & (first - 1)) != 0) {
-      asm volatile("");  // a branch, not both sides
-      const T all = wave_max(key == most_key ? v : gone);
-      first = __ballot(v == all);
+    for (int n = V - 1; n > 0; --n)
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        const bool swap = c[i + 1] > c[i];  // never with one that is gone: those come last or are all
+        const T a = c[i], b = c[i + 1];
+        const int f = e[i], g = e[i + 1];
+        c[i] = swap ? b : a;
+        c[i + 1] = swap ? a : b;
+        e[i] = swap ? g : f;
+        e[i + 1] = swap ? f : g;
+      }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      key[i] = order_key(c[i]);
+      if constexpr (WIDE) {
+        const uint32_t u = (uint32_t)__builtin_bit_cast(uint64_t, c[i]);
+        low[i] = key[i] >> 31 ? u : ~u;
+      }
     }
-    const int winner = __ffsll((unsigned long long)first) - 1;
-    const int e = __builtin_amdgcn_readlane(e0 + at, winner);
+    for (int j = 0; j < s.top; ++j) {
+      const uint32_t most_key = fold_wave(key[0], bits_max);
+      uint64_t first = __ballot(key[0] == most_key);
+      if (WIDE && (first & (first - 1)) != 0) {
+        asm volatile("");  // a branch, not both sides
+        const uint32_t most_low = fold_wave(key[0] == most_key ? low[0] : 0u, bits_max);
+        first &= __ballot(low[0] == most_low);
+      }
+      const int winner = __ffsll((unsigned long long)first) - 1;
+      const int taken = __builtin_amdgcn_readlane(e[0], winner);
+      const bool here = lane == winner;
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (lane == winner && i == at) c[i] = gone;
-    if (lane == j) id = e;
+      for (int i = 0; i < V; ++i) {
+        if (i + 1 < V) {
+          const uint32_t k = key[i], next = key[i + 1];
+          key[i] = here ? next : k;
+          if constexpr (WIDE) {
+            const uint32_t l0 = low[i], l1 = low[i + 1];
+            low[i] = here ? l1 : l0;
+          }
+          const int f = e[i], g = e[i + 1];
+          e[i] = here ? g : f;
+        } else {
+          key[i] = here ? 0u : key[i];  // gone
+        }
+      }
+      if (lane == j) id = taken;
+    }
+  } else {
+    for (int j = 0; j < s.top; ++j) {
+      T v = c[0];
+#pragma unroll
+      for (int i = 1; i < V; ++i) v = larger(v, c[i]);
+      int at = 0;  // the first of this lane's with that value
+#pragma unroll
+      for (int i = V - 1; i >= 0; --i)
+        if (c[i] == v) at = i;
+      // 32 bits of each lane's best are compared; all of them only where those are equal
+      const uint32_t key = order_key(v);
+      uint32_t most_key = fold_wave(key, bits_max);
+      uint64_t first = __ballot(key == most_key);
+      if (WIDE && (first & (first - 1)) != 0) {
+        asm volatile("");  // a branch, not both sides
+        const T all = wave_max(key == most_key ? v : gone);
+        first = __ballot(v == all);
+      }
+      const int winner = __ffsll((unsigned long long)first) - 1;
+      const int e = __builtin_amdgcn_readlane(e0 + at, winner);
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (lane == winner && i == at) c[i] = gone;
+      if (lane == j) id = e;
+    }
   }
 
   double won = 0.0;
