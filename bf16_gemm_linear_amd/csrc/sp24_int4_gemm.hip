@@ -7,6 +7,8 @@
 // us and in parentheses expected, eight weights in turn: 16 x 4096 x 14336 15.6 (14.8), 16 x 14336 x 4096 13.4 (11.7),
 // 32 17.6 (15.3), 64 x 4096 x 14336 27 (28), 128 40 (47); tiled: 256 x 14336 x 4096 58 (68), 2047 x 28672 x 8192 994
 // (1028), where the slab kernel would take 88 and 2400.
+#include <math.h>
+
 #include "sp24_int4.hpp"
 
 namespace sp24 {
@@ -93,30 +95,34 @@ bool int4_experts_by_pairs(int64_t tokens, int64_t pairs, int64_t experts, int64
 }
 
 // An expert product's kernel, by its expected time: `rows` rows of W an expert (gated: gate and up rows), k values.
-// Half of each expert's last tile is taken to be empty.  Measured for 64 experts of 4096 x 1792, 8 a token, gated
-// and down in us:
+// An expert with p tiles' rows on average has p + 1/2 tiles, or one, and in between a little more, since the experts'
+// shares differ.  Scales that come every 32 values (groups below 128) make the slab kernel's steps 1.35 (tiles of 32) to
+// 1.6 times as long; a second round of 256 x 256 tiles takes its time however few they are.  Measured for 64 experts
+// of 4096 x 1792, 8 a token, gated and down in us:
 //   pairs an expert   slab, tiles of 16   slab, tiles of 32   128 x 128 tiles   256 x 256 tiles
-//   8                   126 + 69            161 + 82            394 + 202
-//   16                  182 + 95            186 + 106           397 + 208
-//   37                  -                   329 + 167           289 + 167         352 + 198
-//   75                  -                   571 + 279           349 + 210         376 + 221
-//   150                 -                   1049 + 498          532 + 332         467 + 312
-//   222                 -                   1515 + 691          671 + 379         600 + 350
+//   8                   132 + 82            162 + 84            237 + 124         296 + 148
+//   16                  185 + 105           188 + 108           239 + 126         297 + 151
+//   37                  356 + 212           306 + 162           260 + 137         306 + 159
+//   75                  655 + 379           508 + 260           322 + 176         337 + 180
+//   150                 1192 + 650          932 + 468           493 + 279         455 + 265
+//   222                 -                   -                   664 + 367         591 + 338
+// A tile's step of 64 values costs a part for W and one for each 64 rows that it multiplies.
 struct ExpertsPlan {
   int slab, tiled;  // tokens / 16 of a slab workgroup, or 0 and a tiled configuration
 };
 ExpertsPlan experts_plan(const Pairs& p, int64_t rows, int64_t k, int group) {
   const double pairs = (double)p.count, used = pairs < p.experts ? pairs : p.experts;
   auto tiles = [&](int bm) {
-    const double t = pairs / bm + 0.5 * used;
-    return t > used ? t : used;
+    const double full = pairs / bm / used, over = full - 0.5;
+    return used * 0.5 * (1.5 + full + sqrt(over * over + 0.04));
   };
   const double hbm = used * rows * k / 2 / 5e6;
   double least = 1e30;
   ExpertsPlan best{1, 0};
   for (int mb = 1; mb <= 2; ++mb) {
     const double wg = tiles(16 * mb) * up(rows, 64), few = wg < kCus ? kCus / wg : 1;
-    const double compute = tiles(16 * mb) * up(rows, 32) * up(k, 128) / kCus * (mb == 1 ? 0.13 : 0.2) * few;
+    const double compute = tiles(16 * mb) * up(rows, 32) * up(k, 128) / kCus * few *
+                           (mb == 1 ? 0.13 * (group == 128 ? 1 : 1.6) : 0.2 * (group == 128 ? 1 : 1.35));
     const double t = 3 + (compute > hbm ? compute : hbm);
     if (t < least) {
       least = t;
@@ -125,8 +131,10 @@ ExpertsPlan experts_plan(const Pairs& p, int64_t rows, int64_t k, int group) {
   }
   const double slower = group == 128 ? 1 : group == 64 ? 1.1 : 1.27;  // the sums' rescaling
   const double small = tiles(128) * up(rows, 128), large = tiles(256) * up(rows, 256), steps = (double)up(k, 64) * slower;
-  const double t2 = 4 + (small <= kCus ? 1.0 : 1.4 * (small < 2 * kCus ? 1 : small / (2 * kCus))) * steps;
-  const double t0 = 4 + 1.95 * (large < kCus ? 1 : large / kCus) * steps;
+  const double t2 = 4 + (0.55 + 0.46 * tiles(64) / tiles(128)) *
+                            (small <= kCus ? 0.7 : small < 2 * kCus ? 1 : small / (2 * kCus)) * steps;
+  const double t0 = 4 + (0.98 + 0.33 * tiles(64) / tiles(256)) *
+                            (large <= kCus ? 1 : large < 1.6 * kCus ? 1.6 : large / kCus) * steps;
   if (t2 < least) {
     least = t2;
     best = ExpertsPlan{0, 1};
