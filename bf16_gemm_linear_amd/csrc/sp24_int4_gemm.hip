@@ -5,7 +5,7 @@
 // t = 0.1 for tiles of 16 tokens and 0.14 for 32, steps in whole rounds of W over 256 CUs.
 // Tiled kernel: 4 + rounds * steps of 64 values * t, t by tile.  Measured beside it (HIP graphs):
 // us and in parentheses expected, eight weights in turn: 16 x 4096 x 14336 15.6 (14.8), 16 x 14336 x 4096 13.4 (11.7),
-// 32 17.6 (15.3), 64 x 4096 x 14336 27 (28), 128 40 (47); tiled: 256 x 14336 x 4096 58 (68), 2047 x 28672 x 8192 994
+// 32 17.6 (15.3), 64 x 4096 x 14336 27 (28), 128 40 (47); tiled: 256 x 14336 x 4096 58 (55), 2047 x 28672 x 8192 994
 // (1028), where the slab kernel would take 88 and 2400.
 #include <math.h>
 
@@ -55,7 +55,8 @@ double tiled_plan(int64_t m, int64_t n, int64_t k, int& cfg) {
   const double steps = (double)up(k, 64);
   const int64_t large = up(m, 256) * up(n, 256), small = up(m, 128) * up(n, 128);
   const double t0 = 4 + up(large, kCus) * steps * 2.0;
-  const double t2 = 4 + (small <= kCus ? 1.0 : up(small, 2 * kCus) * 1.47) * steps;
+  // alone on a CU 55 us for k = 4096 (160 x 14336 x 4096, where the slab kernel takes 78)
+  const double t2 = 4 + (small <= kCus ? 0.8 : up(small, 2 * kCus) * 1.47) * steps;
   cfg = t0 < t2 ? 0 : 1;
   return t0 < t2 ? t0 : t2;
 }
@@ -96,8 +97,8 @@ bool int4_experts_by_pairs(int64_t tokens, int64_t pairs, int64_t experts, int64
 
 // An expert product's kernel, by its expected time: `rows` rows of W an expert (gated: gate and up rows), k values.
 // An expert with p tiles' rows on average has p + 1/2 tiles, or one, and in between a little more, since the experts'
-// shares differ.  Scales that come every 32 values (groups below 128) make the slab kernel's steps 1.35 (tiles of 32) to
-// 1.6 times as long; a second round of 256 x 256 tiles takes its time however few they are.  Measured for 64 experts
+// shares differ.  Scales that come every 32 values (groups below 128) make the slab kernel's steps 1.35 (tiles of 32)
+// to 1.6 times as long; a second round of 256 x 256 tiles takes its time however few they are.  Measured for 64 experts
 // of 4096 x 1792, 8 a token, gated and down in us:
 //   pairs an expert   slab, tiles of 16   slab, tiles of 32   128 x 128 tiles   256 x 256 tiles
 //   8                   132 + 82            162 + 84            237 + 124         296 + 148
@@ -130,7 +131,8 @@ ExpertsPlan experts_plan(const Pairs& p, int64_t rows, int64_t k, int group) {
     }
   }
   const double slower = group == 128 ? 1 : group == 64 ? 1.1 : 1.27;  // the sums' rescaling
-  const double small = tiles(128) * up(rows, 128), large = tiles(256) * up(rows, 256), steps = (double)up(k, 64) * slower;
+  const double steps = (double)up(k, 64) * slower;
+  const double small = tiles(128) * up(rows, 128), large = tiles(256) * up(rows, 256);
   const double t2 = 4 + (0.55 + 0.46 * tiles(64) / tiles(128)) *
                             (small <= kCus ? 0.7 : small < 2 * kCus ? 1 : small / (2 * kCus)) * steps;
   const double t0 = 4 + (0.98 + 0.33 * tiles(64) / tiles(256)) *
