@@ -575,7 +575,8 @@ the best first, from logits bf16 or fp32 [tokens, experts].
 Scores are the softmax (ROUTE_SOFTMAX, the default kind) or the sigmoid (ROUTE_SIGMOID) of the
 logits; `bias` (fp32 [experts]) is added for the choice alone.  groups > 1: only experts of the
 top_groups groups whose group_best best experts sum to most.  renormalise: the chosen scores are
-divided by their sum.  Weights are times factor.  Ties go to the lower index; -inf masks an expert.)"),
+divided by their sum.  Weights are times factor.  Ties go to the lower index; -inf or NaN masks an expert: it comes last,
+with weight 0.)"),
     method<g_experts>(R"(experts_int4(x, ids, weights, gu_codes, gu_scales, down_codes, down_scales, gu_zeros=None, down_zeros=None, out=None, ws=None)
 --
 

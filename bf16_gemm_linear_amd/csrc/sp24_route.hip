@@ -2,8 +2,8 @@
 // limit to the best groups of experts, the best `top` of what is left and their weights.
 //
 //   score_i = softmax(l)_i or sigmoid(l_i);   choice c_i = score_i + bias_i, without a bias l_i itself
-//   (both scores rise with l);   c_i = -inf where l_i is -inf or NaN: such an expert is taken last, in
-//   the order of the indices, and with a -inf its weight is 0.
+//   (both scores rise with l).   A NaN counts as -inf: c_i = -inf and score 0, so that such an expert is
+//   taken last, in the order of the indices, with weight 0, and the others' scores do not know of it.
 // Scores that are compared (with a bias, or summed for a group) are formed in 64 bits: among hundreds of
 // experts two fp32 scores within a rounding of each other are met every few thousand tokens, and the
 // choice would depend on the rounding.  Without them the logits are compared, in fp32, as they are.
@@ -23,7 +23,10 @@
 namespace sp24 {
 namespace {
 
-constexpr float kMaxLogit = 3.402823466e38f;  // +inf counts as this
+// A logit as it counts: +inf as the largest number, NaN as -inf.
+__device__ __forceinline__ float logit(float v) {
+  return v != v ? -__builtin_inff() : v > 3.402823466e38f ? 3.402823466e38f : v;
+}
 
 // The unsigned numbers whose order is that of a double's upper word or of a float (no NaN: the least; no -0).
 __device__ __forceinline__ uint32_t order_key(uint32_t bits, bool number) {
@@ -104,7 +107,7 @@ __device__ __forceinline__ void step_two(T& best, T& second) {
   second = larger(a < b ? a : b, larger(c, d));
 }
 
-// e^x to about 2^-51, x <= 0 (below -745: 0; NaN stays one): x = k ln 2 + r, the series of e^r to its
+// e^x to about 2^-51, x <= 0 (below -745: 0): x = k ln 2 + r, the series of e^r to its
 // fourteenth term (|r| <= 0.347: the next is below 2^-57).  All V together: the coefficients are loaded once.
 template <int V>
 __device__ __forceinline__ void exps_of(double (&x)[V]) {
@@ -185,11 +188,11 @@ __global__ __launch_bounds__(256) void route_kernel(sp24_router r, Shape s, int6
   float most = none;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    l[i] = l[i] != l[i] ? __builtin_nanf("") : l[i] > kMaxLogit ? kMaxLogit : l[i];  // every NaN a quiet one
-    most = larger(most, l[i]);  // passes over a NaN
+    l[i] = logit(l[i]);
+    most = larger(most, l[i]);
   }
   if (soft) most = wave_max(most);
-  // a row without numbers has no e^(l - most); its scores are 0 (or NaN)
+  // a row without numbers has no e^(l - most); its scores are 0
   const float from = most == none ? 0.0f : most;
 
   T c[V];
@@ -214,10 +217,10 @@ __global__ __launch_bounds__(256) void route_kernel(sp24_router r, Shape s, int6
     for (int i = 0; i < V; ++i) {
       const double score = c[i];
       c[i] = bias != nullptr && i < held ? score + (double)bias[e0 + i] : (double)l[i];
-      if (!(l[i] > none) || c[i] != c[i]) c[i] = none;  // masked
+      if (!(l[i] > none) || c[i] != c[i]) c[i] = none;  // masked, or a bias that is NaN
       // the group's value is of choices, without a bias of scores
       const double v = bias != nullptr ? c[i] : score;
-      if (c[i] != none && v == v) {
+      if (c[i] != none) {
         second = larger(second, best < v ? best : v);
         best = larger(best, v);
       }
@@ -361,7 +364,7 @@ __global__ __launch_bounds__(256) void route_kernel(sp24_router r, Shape s, int6
   if (mine)
     at = BF16 ? bf16_to_f32(static_cast<const uint16_t*>(logits)[row + id])
               : static_cast<const float*>(logits)[row + id];
-  at = at != at ? __builtin_nanf("") : at > kMaxLogit ? kMaxLogit : at;
+  at = logit(at);
   if (soft) {
     // renormalised: relative to the largest that was chosen, so that none of them underflows
     const float big = r.renormalise ? wave_max(at) : from;

@@ -604,7 +604,8 @@ typedef enum sp24_route_kind { SP24_ROUTE_SOFTMAX = 0, SP24_ROUTE_SIGMOID = 1 } 
 /* A router: which experts a row of logits l stands for, and with which weights.
  *   score_i  = softmax(l)_i or sigmoid(l_i);
  *   choice_i = score_i + bias_i, without a bias l_i itself; -inf where l_i is -inf (a
- *              masked expert) or a NaN;
+ *              masked expert: score 0) or a NaN, which counts as -inf in all of this, or
+ *              where bias_i is a NaN;
  *   groups > 1: the experts are that many groups of experts / groups neighbours; a
  *              group's value is the sum of its group_best (1 or 2) largest choices
  *              (without a bias and with group_best 2, scores), masked ones left out,

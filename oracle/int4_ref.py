@@ -78,27 +78,24 @@ def route(logits, top, sigmoid=False, bias=None, groups=1, top_groups=1, group_b
     tokens, experts = l.shape
     ids, weights = np.zeros((tokens, top), np.int32), np.zeros((tokens, top))
     for t in range(tokens):
-        row = np.minimum(l[t], np.finfo(np.float32).max)  # keeps a NaN
+        row = np.minimum(np.where(np.isnan(l[t]), -np.inf, l[t]), np.finfo(np.float32).max)
         masked = np.isneginf(row)
         with np.errstate(all="ignore"):
             if sigmoid:
                 score = 1.0 / (1.0 + np.exp(-row))
             else:
-                numbers = row[~np.isnan(row)]
-                score = np.exp(row - (numbers.max() if numbers.size else 0.0))
-                score = np.where(masked, 0.0, score)
+                score = np.exp(row - (0.0 if masked.all() else row.max()))
                 score = score / score.sum() if score.sum() != 0 else np.zeros(experts)
         score = np.where(masked, 0.0, score)
         choice = row if bias is None else score + np.asarray(bias, np.float64)
-        choice = np.where(masked | np.isnan(row) | np.isnan(choice), -np.inf, choice)
+        choice = np.where(masked | np.isnan(choice), -np.inf, choice)
         allowed = np.ones(experts, bool)
         if groups > 1:
             n = experts // groups
             value = np.full(groups, -np.inf)
             for g in range(groups):
                 of = score if bias is None and group_best == 2 else choice
-                there = [v for v, c in zip(of[g * n:(g + 1) * n], choice[g * n:(g + 1) * n])
-                         if c != -np.inf and not np.isnan(v)]
+                there = [v for v, c in zip(of[g * n:(g + 1) * n], choice[g * n:(g + 1) * n]) if c != -np.inf]
                 if there:
                     value[g] = sum(sorted(there)[-group_best:])
             best = sorted(range(groups), key=lambda g: (-value[g], g))[:top_groups]
@@ -109,9 +106,7 @@ def route(logits, top, sigmoid=False, bias=None, groups=1, top_groups=1, group_b
             with np.errstate(all="ignore"):
                 if not sigmoid:  # the softmax over those chosen
                     at = row[order]
-                    known = at[~np.isnan(at)]
-                    big = known.max() if known.size else 0.0
-                    w = np.where(np.isneginf(at), 0.0, np.exp(at - big))
+                    w = np.exp(at - (0.0 if np.isneginf(at).all() else at.max()))
                 w = w / w.sum() if w.sum() != 0 else np.zeros(top)
         ids[t], weights[t] = order, w * factor
     return ids, weights
