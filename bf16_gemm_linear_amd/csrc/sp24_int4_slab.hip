@@ -13,10 +13,9 @@
 // 32; accumulator register e is token 4 (l / 16) + e, W row l % 16.  A lane loads 16 bytes of codes, block
 // l / 16 of its row's four; a transposition of the 4 x 4 words of lanes l, l + 16, l + 32, l + 48 (four
 // register exchanges) gives it word l / 16 of every block, so each instruction covers one block of 32 and
-// any group size works.  Codes become the bf16 pairs (128 + q); what that adds is taken off again: without zero
-// points the sums start from those of -136 x, one more instruction for all the workgroup's columns, and with
-// them (128 + z) times the sum of x, from an instruction with ones, in fp32 behind a group's sum.  Rows past the last
-// are the last one again; their outputs are not stored.
+// any group size works.  Codes become the bf16 pairs c + q - z; the sums of c x, one more instruction for all
+// the workgroup's columns, are taken off behind a group's sum.  Rows past the last are the last one again; their
+// outputs are not stored.
 //
 // 16 x 4096 x 14336 with zero points takes 12.4 to 13.4 us and 2.8 to 3.9 for the join (14.1 a call), 16 x 14336 x
 // 4096 11.6; what is left over the weight's 6 is X, a launch and its end.  77 x 6144 x 4096 by groups of 32
@@ -64,7 +63,7 @@ __global__ __launch_bounds__(1024, 4) void int4_slab_kernel(Args p) {
   constexpr int H = MODE == GATED ? 2 : 1, OB = RB / H;  // gate rows and up rows; row blocks of the output
   static_assert(OB > 0, "GATED needs a gate and an up block");
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  uint32_t* const sz = reinterpret_cast<uint32_t*>(lds + p.xbytes);  // scale and zero of (row, group): bf16, byte
+  uint32_t* const sz = reinterpret_cast<uint32_t*>(lds + p.xbytes);  // scale and zero of (row, group): bf16, Int4Zeros
   const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), waves = p.cbs * p.kp;
   const int cb = wave % p.cbs, kw = wave / p.cbs;
@@ -103,8 +102,8 @@ __global__ __launch_bounds__(1024, 4) void int4_slab_kernel(Args p) {
 #pragma unroll
     for (int j = 0; j < MB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   const f32x4 zero{0.f, 0.f, 0.f, 0.f};
-  const Int4Bits bits;
-  constexpr uint32_t all = Z ? 0x3F803F80u : 0xC308C308u;  // pairs of 1, or of -136
+  const Int4Bits<Z> bits;
+  constexpr uint32_t all = Int4Bits<Z>::kConstant;
   const bf16x8 constant = __builtin_bit_cast(bf16x8, u32x4{all, all, all, all});
 
   for (int k0 = kbegin; k0 < kend; k0 += p.chunk) {
@@ -135,66 +134,55 @@ __global__ __launch_bounds__(1024, 4) void int4_slab_kernel(Args p) {
       // row block i's scale words: gate rows come before the workgroup's up rows
       auto both = [&](int i, int g) { return szr[(16 * (i % OB) + (i < OB ? 0 : cols)) * stride + g]; };
       bf16x8 b[RB][4];  // of every block
-      float sc[RB][G128 ? 1 : 4], zp[RB][G128 ? 1 : 4];
+      float sc[RB][G128 ? 1 : 4], times[RB][G128 ? 1 : 4];  // of c x
 #pragma unroll
       for (int i = 0; i < RB; ++i) {
-        uint32_t w[4] = {wq[i][0], wq[i][1], wq[i][2], wq[i][3]};
+        uint32_t w[4] = {wq[i][0], wq[i][1], wq[i][2], wq[i][3]}, z = 0;
         transpose4(w);
 #pragma unroll
-        for (int d = 0; d < 4; ++d) b[i][d] = bits.values(w[d]);
-#pragma unroll
-        for (int d = 0; d < (G128 ? 1 : 4); ++d) {
-          // past the row's end (a last step of fewer than four blocks): unused
-          const uint32_t s = both(i, G128 ? 0 : min(d >> gshift, gc - 1 - (4 * step >> gshift)));
-          sc[i][d] = __uint_as_float(s & 0xFFFF0000u);
-          zp[i][d] = Z ? 128.0f + (float)(s & 255u) : 0.0f;
+        for (int d = 0; d < 4; ++d) {
+          if (d == 0 || !G128) {
+            // past the row's end (a last step of fewer than four blocks): unused
+            const uint32_t s = both(i, G128 ? 0 : min(d >> gshift, gc - 1 - (4 * step >> gshift)));
+            sc[i][d] = __uint_as_float(s & 0xFFFF0000u);
+            if constexpr (Z) {
+              z = Int4Zeros::bytes(s);
+              times[i][d] = Int4Zeros::times(s);
+            }
+          }
+          b[i][d] = bits.values(w[d], z);
         }
       }
       const int left = blocks - 4 * step;  // G128: at least four
 #pragma unroll
       for (int j = 0; j < MB; ++j) {
-        // a group's sums of this row block's columns, of x times the constant `sx`
-        auto add = [&](int i, int d, const f32x4& v, const f32x4& sx) {
+        // a group's sums of this row block's columns, and of c x
+        auto add = [&](int i, int d, const f32x4& v, const f32x4& cx) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][j][e] += sc[i][d] * (Z ? v[e] - zp[i][d] * sx[e] : v[e]);
+          for (int e = 0; e < 4; ++e) acc[i][j][e] += sc[i][d] * (Z ? v[e] - times[i][d] * cx[e] : v[e] - cx[e]);
         };
         if constexpr (G128) {
-          // 16 tokens: the step's X stays in registers, and the columns' sums start from sx; for 32 there is no room
-          constexpr bool KEEP = MB == 1;
-          bf16x8 a[KEEP ? 4 : 1];
-          f32x4 v[RB], sx = zero;
+          f32x4 v[RB], cx = zero;
 #pragma unroll
           for (int i = 0; i < RB; ++i) v[i] = zero;
-          auto columns = [&](int d, const bf16x8& x) {
-#pragma unroll
-            for (int i = 0; i < RB; ++i) v[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, b[i][d], v[i], 0, 0, 0);
-          };
 #pragma unroll
           for (int d = 0; d < 4; ++d) {
-            a[KEEP ? d : 0] = x(j, d);
-            sx = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[KEEP ? d : 0], constant, sx, 0, 0, 0);
-            if constexpr (!KEEP) columns(d, a[0]);
-          }
-          if constexpr (KEEP) {
+            const bf16x8 a = x(j, d);
+            cx = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, constant, cx, 0, 0, 0);
 #pragma unroll
-            for (int i = 0; i < RB; ++i) v[i] = Z ? zero : sx;
-#pragma unroll
-            for (int d = 0; d < 4; ++d) columns(d, a[d]);
-          } else if constexpr (!Z) {
-#pragma unroll
-            for (int i = 0; i < RB; ++i) v[i] += sx;
+            for (int i = 0; i < RB; ++i) v[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b[i][d], v[i], 0, 0, 0);
           }
 #pragma unroll
-          for (int i = 0; i < RB; ++i) add(i, 0, v[i], sx);
+          for (int i = 0; i < RB; ++i) add(i, 0, v[i], cx);
         } else {
 #pragma unroll
           for (int d = 0; d < 4; ++d) {
             if (d >= left) break;  // uniform
             const bf16x8 a = x(j, d);
-            const f32x4 sx = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, constant, zero, 0, 0, 0);
+            const f32x4 cx = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, constant, zero, 0, 0, 0);
 #pragma unroll
             for (int i = 0; i < RB; ++i)
-              add(i, d, __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b[i][d], Z ? zero : sx, 0, 0, 0), sx);
+              add(i, d, __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b[i][d], zero, 0, 0, 0), cx);
           }
         }
       }
@@ -232,7 +220,7 @@ __global__ __launch_bounds__(1024, 4) void int4_slab_kernel(Args p) {
         }
 #pragma unroll
         for (int f = 0; f < F; ++f)
-          if (row + f * per < H * cols) sz[(row + f * per) * stride + g] = fs[f] << 16 | fz[f];
+          if (row + f * per < H * cols) sz[(row + f * per) * stride + g] = fs[f] << 16 | Int4Zeros::of(fz[f]);
       }
     }
     __builtin_amdgcn_sched_barrier(0);

@@ -5,14 +5,14 @@
 // row's load is 1 KB of neighbouring bytes, and the lane's x stays in registers for all rows.  No LDS
 // before the end, no waits between waves: what is in flight at once is a decode step's whole share of
 // W (n = 14336, k = 4096: 14 waves a CU of 8 KB each).
-// Two values at a time: (128 + q) as bf16 pairs (shift, and-or), then v_dot2_f32_bf16, 11
-// instructions for 8 values and one token.  A group's scale and zero come in behind the block's sum:
-// s (sum x (128 + q) - (128 + z) sum x), in fp32; a block of 32 lies in one group.
+// Two values at a time: c + q - z as bf16 pairs (shift, and-or; with zero points their bytes), then
+// v_dot2_f32_bf16, 11 instructions for 8 values and one token, or 13.  The sum of c x and the group's scale come in
+// behind the block's sum, in fp32; a block of 32 lies in one group.
 // The lanes' sums are joined by register exchanges (rows and lanes transposed on the way), those of
 // the chunks through LDS, in a fixed order.
 //
 // One token of 14336 x 4096 (30.3 MB) takes 6.7 to 7.6 us (4.0 to 4.5 TB/s; a copy reaches 5.17), a call after
-// another 7.6; two tokens 10.4 in a graph, as many again of the 11 instructions.  The experts' block of one
+// another 7.6; two tokens 8.9 in a graph, as many again of the products.  The experts' block of one
 // token, 8 of 64 experts of 4096 x 1792: gated 12.9 to 13.8 us (60 MB: 4.4 to 4.7 TB/s), down 7.6 to 8.5.  8 rows a
 // workgroup: with 4 each lane's x would be read twice as often; 16 leave fewer waves than fill the CUs.
 #include "sp24_int4.hpp"
@@ -59,7 +59,7 @@ __device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float c) {
 constexpr int RB = 8;  // rows of W a workgroup (GATED: half of them gate rows, half their up rows)
 
 // MT tokens.
-template <int MT, int MODE, int OCC>
+template <int MT, int MODE, int OCC, bool Z>
 __global__ __launch_bounds__(512, OCC) void int4_vec_kernel(Args p) {
   constexpr int OUT = MODE == GATED ? RB / 2 : RB;  // outputs a workgroup
   __shared__ float red[8][RB * MT];
@@ -78,7 +78,7 @@ __global__ __launch_bounds__(512, OCC) void int4_vec_kernel(Args p) {
     expert = id;
   }
 
-  const Int4Bits bits;
+  const Int4Bits<Z> bits;
   float acc[RB][MT];
 #pragma unroll
   for (int r = 0; r < RB; ++r)
@@ -103,6 +103,16 @@ __global__ __launch_bounds__(512, OCC) void int4_vec_kernel(Args p) {
     }
     const int b = chunk * 64 + lane, kb = min(b, blocks - 1);
 
+    // All loads before the first product; X's first, since loads arrive in order and a row of W is multiplied while
+    // the rows behind it are on their way.
+    u32x4 x[MT][4];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      const size_t tok = MODE == PLAIN ? t : 0;
+      const u32x4* xp = reinterpret_cast<const u32x4*>(xr + tok * p.k + (size_t)kb * 32);
+#pragma unroll
+      for (int d = 0; d < 4; ++d) x[t][d] = xp[d];
+    }
     u32x4 w[RB];
     uint32_t s[RB], z[RB];
 #pragma unroll
@@ -112,41 +122,38 @@ __global__ __launch_bounds__(512, OCC) void int4_vec_kernel(Args p) {
       w[r] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p.w.codes + row * half) + kb);
       const size_t g = row * groups + (kb >> gshift);
       s[r] = p.w.scales[g];
-      z[r] = p.w.zeros == nullptr ? kInt4Zero : p.w.zeros[g];
+      z[r] = Z ? p.w.zeros[g] : 0;
     }
-    uint32_t x[MT][16];
-    float sx[MT];
+    __builtin_amdgcn_sched_barrier(0);
+    float cx[MT];
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
-      const size_t tok = MODE == PLAIN ? t : 0;
-      const u32x4* xp = reinterpret_cast<const u32x4*>(xr + tok * p.k + (size_t)kb * 32);
-      sx[t] = 0.0f;
-#pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        const u32x4 v = xp[d];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[t][4 * d + i] = b < blocks ? v[i] : 0u;  // past the row: nothing is added
-          sx[t] = dot2(0x3F803F80u, x[t][4 * d + i], sx[t]);
-        }
-      }
-    }
-#pragma unroll
-    for (int r = 0; r < RB; ++r) {
-      float sum[MT];
-#pragma unroll
-      for (int t = 0; t < MT; ++t) sum[t] = 0.0f;
+      cx[t] = 0.0f;
 #pragma unroll
       for (int d = 0; d < 4; ++d)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t q = bits.pair(w[r][d], i);
-#pragma unroll
-          for (int t = 0; t < MT; ++t) sum[t] = dot2(q, x[t][4 * d + i], sum[t]);
+          x[t][d][i] = b < blocks ? x[t][d][i] : 0u;  // past the row: nothing is added
+          cx[t] = dot2(Int4Bits<Z>::kConstant, x[t][d][i], cx[t]);
         }
-      const float scale = bf16_to_f32(s[r]) * weight, zp = 128.0f + (float)z[r];
+    }
 #pragma unroll
-      for (int t = 0; t < MT; ++t) acc[r][t] += scale * (sum[t] - zp * sx[t]);
+    for (int r = 0; r < RB; ++r) {
+      const uint32_t zero = Z ? Int4Zeros::of(z[r]) : 0, zp = Z ? Int4Zeros::bytes(zero) : 0;
+      float sum[MT];
+#pragma unroll
+      for (int t = 0; t < MT; ++t) sum[t] = 0.0f;
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        const u32x4 q = __builtin_bit_cast(u32x4, bits.values(w[r][d], zp));
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int t = 0; t < MT; ++t) sum[t] = dot2(q[i], x[t][d][i], sum[t]);
+      }
+      const float scale = bf16_to_f32(s[r]) * weight, times = Z ? Int4Zeros::times(zero) : 1.0f;
+#pragma unroll
+      for (int t = 0; t < MT; ++t) acc[r][t] += scale * (Z ? sum[t] - times * cx[t] : sum[t] - cx[t]);
     }
   }
 
@@ -184,7 +191,9 @@ hipError_t launch(Args a, int64_t items, hipStream_t s) {
   a.kw = work < 8 ? work : 8;
   const int64_t grid = items * ((a.n + OUT - 1) / OUT);
   if (grid * 64 * a.kw >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;  // HIP counts threads in 32 bits
-  hipLaunchKernelGGL((int4_vec_kernel<MT, MODE, OCC>), dim3((uint32_t)grid), dim3(64 * a.kw), 0, s, a);
+  const dim3 g((uint32_t)grid), block(64 * a.kw);
+  if (a.w.zeros != nullptr) hipLaunchKernelGGL((int4_vec_kernel<MT, MODE, OCC, true>), g, block, 0, s, a);
+  else hipLaunchKernelGGL((int4_vec_kernel<MT, MODE, OCC, false>), g, block, 0, s, a);
   return hipGetLastError();
 }
 

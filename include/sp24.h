@@ -584,10 +584,12 @@ int sp24_dequant_int4(const uint8_t* codes, const void* scales_bf16, const uint8
                       int64_t group, void* out_bf16, void* stream);
 
 /* Y = X . W^T, X bf16 [m, k], W [n, k] as above, Y bf16 [m, n].  Sums over a group in
- * fp32 of x * (q - z), which is exact in each product; times s and summed over the
- * groups in fp32; rounded once.  The order of the sums is fixed for a given (m, n, k):
- * results are bitwise reproducible.  A token with an Inf or a NaN has Inf or NaN in
- * its row of Y, and only there.  Magnitudes of X up to 2^112 and of scales up to 2^119.
+ * fp32, times s and summed over the groups in fp32; rounded once.  A group's sum is that
+ * of x * (q - z), or for few tokens the difference of the sums of x * (c + q - z) and
+ * of c * x, c = 136 (192 with zeros): exact in each product, and where q = z in all of
+ * a group it adds exactly nothing.  The order of the sums is fixed for a given
+ * (m, n, k): results are bitwise reproducible.  A token with an Inf or a NaN has Inf or
+ * NaN in its row of Y (which of them depends on the form of the sums), and only there.  Magnitudes of X up to 2^112 and of scales up to 2^119.
  * Requires m, n >= 1, at most 2^21; group <= k <= 2^20.
  *   ws/ws_bytes: sp24_gemm_int4_workspace_size(m, n, k), which is 0 outside 3..1024 tokens.
  * (SP24_ERR_HIP where no grid covers the outputs: beyond 2^39 of them.) */
