@@ -9,7 +9,8 @@
 // v_dot2_f32_bf16, 11 instructions for 8 values and one token, or 13.  The sum of c x and the group's scale come in
 // behind the block's sum, in fp32; a block of 32 lies in one group.
 // The lanes' sums are joined by register exchanges (rows and lanes transposed on the way), those of
-// the chunks through LDS, in a fixed order.
+// the chunks through LDS, in a fixed order; the experts' down product keeps the slots of a token apart until each
+// is finished, then adds them in their order, times their weights.
 //
 // One token of 14336 x 4096 (30.3 MB) takes 6.7 to 7.6 us (4.0 to 4.5 TB/s; a copy reaches 5.17), a call after
 // another 7.6; two tokens 8.9 in a graph, as many again of the products.  The experts' block of one
@@ -62,7 +63,11 @@ constexpr int RB = 8;  // rows of W a workgroup (GATED: half of them gate rows, 
 template <int MT, int MODE, int OCC, bool Z>
 __global__ __launch_bounds__(512, OCC) void int4_vec_kernel(Args p) {
   constexpr int OUT = MODE == GATED ? RB / 2 : RB;  // outputs a workgroup
-  __shared__ float red[8][RB * MT];
+  static_assert(MODE == PLAIN || MT == 1, "a pair has one token");
+  constexpr int TOP = 64;  // the most slots of a token that sp24_experts_int4 takes
+  __shared__ float red[MODE == DOWN ? TOP * 8 : 8][RB * MT];  // by wave; DOWN: by slot and wave
+  __shared__ float slot_weight[MODE == DOWN ? TOP : 1];
+  __shared__ int slot_there[MODE == DOWN ? TOP : 1];
   const int tid = threadIdx.x, lane = tid & 63;
   const int kw = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int nblocks = (p.n + OUT - 1) / OUT;
@@ -78,25 +83,50 @@ __global__ __launch_bounds__(512, OCC) void int4_vec_kernel(Args p) {
     expert = id;
   }
 
+  int slot_id = 0;  // DOWN: of slot `tid`, loaded here and looked at behind the products
+  float weight = 0.0f;
+  if constexpr (MODE == DOWN) {
+    if (tid < p.top) {
+      slot_id = p.ids[item * p.top + tid];
+      weight = p.weights[item * p.top + tid];
+    }
+  }
+
   const Int4Bits<Z> bits;
   float acc[RB][MT];
+  auto clear = [&] {
 #pragma unroll
-  for (int r = 0; r < RB; ++r)
+    for (int r = 0; r < RB; ++r)
 #pragma unroll
-    for (int t = 0; t < MT; ++t) acc[r][t] = 0.0f;
+      for (int t = 0; t < MT; ++t) acc[r][t] = 0.0f;
+  };
+  // The lanes' sums, to red[at]: rows 2^0, 2^1, 2^2 go to lane bits 5, 4, 3.
+  auto join = [&](int at) {
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      float v[RB / 2];
+#pragma unroll
+      for (int r = 0; r < RB / 2; ++r) v[r] = merge<32>(acc[2 * r][t], acc[2 * r + 1][t], lane);
+      const float u = merge<8>(merge<16>(v[0], v[1], lane), merge<16>(v[2], v[3], lane), lane);
+      const int row = (lane >> 5 & 1) | (lane >> 4 & 1) << 1 | (lane >> 3 & 1) << 2;
+      const uint32_t f =
+          fold_lanes<4>(fold_lanes<2>(fold_lanes<1>(__float_as_uint(u), bits_sum), bits_sum), bits_sum);
+      if ((lane & (64 / RB - 1)) == 0) red[at][row * MT + t] = __uint_as_float(f);
+    }
+  };
+  clear();
 
+  // DOWN: chunk after chunk of slot after slot, the waves in turn
   const int work = MODE == DOWN ? chunks * p.top : chunks;
   for (int c = kw; c < work; c += p.kw) {
-    int chunk = c;
-    float weight = 1.0f;
+    int chunk = c, slot = 0;
     const uint16_t* xr = p.x;
     if constexpr (MODE == DOWN) {
-      const int slot = c / chunks;
+      slot = c / chunks;
       chunk = c - slot * chunks;
       const int id = p.ids[item * p.top + slot];
       if ((uint32_t)id >= (uint32_t)p.experts) continue;  // uniform
       expert = id;
-      weight = p.weights[item * p.top + slot];
       xr += (size_t)(item * p.top + slot) * p.k;
     } else if constexpr (MODE == GATED) {
       xr += (size_t)(item / p.top) * p.k;
@@ -151,24 +181,52 @@ __global__ __launch_bounds__(512, OCC) void int4_vec_kernel(Args p) {
 #pragma unroll
           for (int t = 0; t < MT; ++t) sum[t] = dot2(q[i], x[t][d][i], sum[t]);
       }
-      const float scale = bf16_to_f32(s[r]) * weight, times = Z ? Int4Zeros::times(zero) : 1.0f;
+      const float scale = bf16_to_f32(s[r]), times = Z ? Int4Zeros::times(zero) : 1.0f;
 #pragma unroll
       for (int t = 0; t < MT; ++t) acc[r][t] += scale * (Z ? sum[t] - times * cx[t] : sum[t] - cx[t]);
     }
+    if constexpr (MODE == DOWN) {
+      if (c + p.kw >= (slot + 1) * chunks) {  // the last of the slot's that this wave has
+        join(slot * 8 + kw);
+        clear();
+      }
+    }
   }
 
-  // rows 2^0, 2^1, 2^2 go to lane bits 5, 4, 3
+  if constexpr (MODE == DOWN) {
+    if (tid < TOP) {
+      slot_weight[tid] = weight;
+      slot_there[tid] = tid < p.top && (uint32_t)slot_id < (uint32_t)p.experts;
+    }
+    __syncthreads();
+    // the slots in their order: each one's product, its chunks in their order, times its weight
+    if (tid < RB) {
+      constexpr int J = 8;  // slots whose values are read together, without branches between
+      const int parts = min(chunks, p.kw);
+      float y = 0.0f;
+#pragma unroll 1
+      for (int j0 = 0; j0 < p.top; j0 += J) {
+        float v[J], w[J];
+        int there[J];
 #pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    float v[RB / 2];
+        for (int i = 0; i < J; ++i) {
+          w[i] = slot_weight[j0 + i];
+          there[i] = slot_there[j0 + i];
+          v[i] = red[(j0 + i) * 8 + ((j0 + i) * chunks & 7)][tid];
+        }
+#pragma unroll 1
+        for (int part = 1; part < parts; ++part)
 #pragma unroll
-    for (int r = 0; r < RB / 2; ++r) v[r] = merge<32>(acc[2 * r][t], acc[2 * r + 1][t], lane);
-    const float u = merge<8>(merge<16>(v[0], v[1], lane), merge<16>(v[2], v[3], lane), lane);
-    const int row = (lane >> 5 & 1) | (lane >> 4 & 1) << 1 | (lane >> 3 & 1) << 2;
-    const uint32_t f =
-        fold_lanes<4>(fold_lanes<2>(fold_lanes<1>(__float_as_uint(u), bits_sum), bits_sum), bits_sum);
-    if ((lane & (64 / RB - 1)) == 0) red[kw][row * MT + t] = __uint_as_float(f);
+          for (int i = 0; i < J; ++i)
+            v[i] += red[(j0 + i) * 8 + (((j0 + i) * chunks + part) & 7)][tid];  // fewer than 8 waves: a chunk each
+#pragma unroll
+        for (int i = 0; i < J; ++i) y += (there[i] != 0 ? w[i] : 0.0f) * (there[i] != 0 ? v[i] : 0.0f);
+      }
+      if (n0 + tid < p.n) p.y[(size_t)item * p.n + n0 + tid] = (uint16_t)f32x2_to_bf16x2(y, 0.0f);
+    }
+    return;
   }
+  join(kw);
   __syncthreads();
   if (tid < OUT * MT) {
     const int t = tid % MT, i = tid / MT;
@@ -178,7 +236,7 @@ __global__ __launch_bounds__(512, OCC) void int4_vec_kernel(Args p) {
       if constexpr (MODE == GATED) u += red[z][(i + OUT) * MT + t];
     }
     if constexpr (MODE == GATED) v = silu_mul(v, u);
-    const int64_t row = MODE == PLAIN ? t : item;
+    const int64_t row = MODE == PLAIN ? t : item;  // GATED: the pair
     if (n0 + i < p.n)
       p.y[(size_t)row * p.n + n0 + i] = (uint16_t)f32x2_to_bf16x2(v, 0.0f);
   }
