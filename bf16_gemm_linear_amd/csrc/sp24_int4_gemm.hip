@@ -8,6 +8,9 @@
 // 32 17.6 (15.3), 64 x 4096 x 14336 27 (28), 128 40 (47); tiled: 256 x 14336 x 4096 58 (55), 2047 x 28672 x 8192 994
 // (1028), where the slab kernel would take 88 and 2400.
 #include <math.h>
+#include <stdio.h>
+#include <stdlib.h>
+#include <string.h>
 
 #include "sp24_int4.hpp"
 
@@ -26,7 +29,7 @@ int slab_chunk(int rows, int wrows, int group) {
   return c;
 }
 
-// The best slab plan and its expected time.  No group here: the workspace's size does not depend on it.
+// The best slab plan and its expected time.
 double slab_plan(int64_t m, int64_t n, int64_t k, SlabPlan& best) {
   double least = 1e30;
   for (int mb = 1; mb <= 2; ++mb) {
@@ -61,37 +64,77 @@ double tiled_plan(int64_t m, int64_t n, int64_t k, int& cfg) {
   return t0 < t2 ? t0 : t2;
 }
 
+enum Kernel { VEC, SLAB, TILED, NONE };
+
+// SP24_INT4="vec", "slab,tokens / 16,waves along the columns,waves along K,slices" or "tiled,configuration" takes that
+// kernel and form where it can run the call; with a "!" after it, it and no other: a call that it cannot run fails
+// (tuning and tests only).
+struct Named {
+  Kernel kernel = NONE;
+  bool only = false;
+  int id = 0, cbs = 0, kp = 0, slices = 1;  // id: tokens / 16 or the tiled configuration
+};
+Named named() {
+  Named r;
+  const char* const v = getenv("SP24_INT4");
+  if (v == nullptr || v[0] == '\0') return r;
+  r.only = v[strlen(v) - 1] == '!';
+  char name[8];
+  const int parts = sscanf(v, "%7[a-z],%d,%d,%d,%d", name, &r.id, &r.cbs, &r.kp, &r.slices);
+  if (parts >= 1 && strcmp(name, "vec") == 0) r.kernel = VEC;
+  if (parts == 2 && strcmp(name, "tiled") == 0 && (r.id == 0 || r.id == 1)) r.kernel = TILED;
+  if (parts == 5 && strcmp(name, "slab") == 0 && (r.id == 1 || r.id == 2) && r.cbs >= 1 && r.kp >= 1 &&
+      r.cbs * r.kp <= 16 && r.slices >= 1 && r.slices <= 8)
+    r.kernel = SLAB;
+  return r;
+}
+
+// A dense product's kernel and form.  No group here: the workspace's size does not depend on it.
+struct Plan {
+  Kernel kernel;
+  SlabPlan slab;
+  int tiled;
+};
+Plan plan(int64_t m, int64_t n, int64_t k) {
+  Plan p{m <= 2 ? VEC : TILED, SlabPlan{}, 0};
+  const Named f = named();
+  if (f.kernel == TILED) return Plan{TILED, SlabPlan{}, f.id};
+  if (f.kernel == SLAB)
+    return Plan{SLAB, SlabPlan{f.id, f.cbs, f.kp, f.slices == 1 ? (int)k : (int)(up(up(k, f.slices), 128) * 128), 0}, 0};
+  if (f.only && (f.kernel != VEC || m > 2)) return Plan{NONE, SlabPlan{}, 0};
+  if (p.kernel == VEC) return p;
+  const double tiled = tiled_plan(m, n, k, p.tiled);
+  if (m <= kSlabTokens && slab_plan(m, n, k, p.slab) <= tiled) p.kernel = SLAB;
+  return p;
+}
+
 }  // namespace
 
 size_t int4_gemm_workspace(int64_t m, int64_t n, int64_t k) {
-  SlabPlan q;
-  int cfg;
-  if (m <= 2 || m > kSlabTokens || slab_plan(m, n, k, q) > tiled_plan(m, n, k, cfg) || q.slice >= k) return 0;
-  return (size_t)up(k, q.slice) * m * n * 4;
+  const Plan p = plan(m, n, k);
+  return p.kernel == SLAB && p.slab.slice < k ? (size_t)up(k, p.slab.slice) * m * n * 4 : 0;
 }
 
 hipError_t launch_int4_gemm(const Int4Gemm& a, float* part, hipStream_t s) {
-  if (a.m <= 2) return launch_int4_vec(a, s);
-  int cfg;
-  const double tiled = tiled_plan(a.m, a.n, a.k, cfg);
-  if (a.m <= kSlabTokens) {
-    SlabPlan q;
-    if (slab_plan(a.m, a.n, a.k, q) <= tiled) {
-      const int fits = slab_chunk(a.m < 16 * q.mb ? a.m : 16 * q.mb, 32 * q.cbs, a.group);
-      q.chunk = q.slice < fits ? q.slice : fits;
-      // Several passes over LDS: three waves a SIMD instead of two hide more of their starts.  With two and three,
-      // us: 77 x 6144 x 4096 by groups of 32 22.0 and 20.2, 96 x 6144 x 4096 by 64 25.6 and 22.5; in one pass by
-      // 128 48 x 14336 x 4096 30.2 and 31.1, 16 x 28672 x 4096 18.5 and 19.5.
-      if (q.cbs == 4 && q.chunk < q.slice) q.kp = 3;
-      return launch_int4_slab(q, a, part, s);
-    }
-  }
-  return launch_int4_tiled(cfg, a, s);
+  Plan p = plan(a.m, a.n, a.k);
+  if (p.kernel == VEC) return launch_int4_vec(a, s);
+  if (p.kernel == TILED) return launch_int4_tiled(p.tiled, a, s);
+  if (p.kernel == NONE) return hipErrorInvalidConfiguration;
+  SlabPlan& q = p.slab;
+  const int fits = slab_chunk(a.m < 16 * q.mb ? a.m : 16 * q.mb, 32 * q.cbs, a.group);
+  q.chunk = q.slice < fits ? q.slice : fits;
+  // Several passes over LDS: three waves a SIMD instead of two hide more of their starts.  With two and three,
+  // us: 77 x 6144 x 4096 by groups of 32 22.0 and 20.2, 96 x 6144 x 4096 by 64 25.6 and 22.5; in one pass by
+  // 128 48 x 14336 x 4096 30.2 and 31.1, 16 x 28672 x 4096 18.5 and 19.5.
+  if (q.cbs == 4 && q.chunk < q.slice && named().kernel == NONE) q.kp = 3;
+  return launch_int4_slab(q, a, part, s);
 }
 
 bool int4_experts_by_pairs(int64_t tokens, int64_t pairs, int64_t experts, int64_t d, int64_t f) {
   const int64_t used = pairs < experts ? pairs : experts;
+  const Named by_name = named();
   const bool grids = pairs * f < (int64_t)1 << 25 && tokens * d < (int64_t)1 << 26;  // HIP counts threads in 32 bits
+  if (by_name.kernel != NONE) return by_name.kernel == VEC && grids;
   return tokens <= 64 && grids && (double)(pairs - used) * d * f * 1.5 <= 25e6;
 }
 
@@ -155,6 +198,14 @@ SlabPlan experts_slab(const ExpertsPlan& e, const Pairs& p, int64_t rows, int64_
 }
 
 hipError_t launch_int4_experts(const Int4Experts& a, hipStream_t s) {
+  const Named f = named();
+  if (f.kernel == TILED || f.kernel == SLAB) {  // both products
+    auto slab = [&](int k) { return SlabPlan{f.id, f.cbs, f.kp, k, k < 2048 / f.id ? k : 2048 / f.id}; };
+    const hipError_t e = f.kernel == TILED ? launch_int4_tiled_gated(f.id, a, s) : launch_int4_slab_gated(slab(a.d), a, s);
+    if (e != hipSuccess) return e;
+    return f.kernel == TILED ? launch_int4_tiled_down(f.id, a, s) : launch_int4_slab_down(slab(a.f), a, s);
+  }
+  if (f.only) return hipErrorInvalidConfiguration;
   const ExpertsPlan g = experts_plan(a.pairs, 2 * (int64_t)a.f, a.d, a.group);
   hipError_t e = g.slab ? launch_int4_slab_gated(experts_slab(g, a.pairs, 2 * (int64_t)a.f, a.d, 4), a, s)
                         : launch_int4_tiled_gated(g.tiled, a, s);
