@@ -4,9 +4,11 @@
 //   3 + max(steps t, HBM) + (X + W through L2) / 26 TB/s + 2.2 + slices (0.3 + a slice's sums through memory),
 // t = 0.1 for tiles of 16 tokens and 0.14 for 32, steps in whole rounds of W over 256 CUs.
 // Tiled kernel: 4 + rounds * steps of 64 values * t, t by tile.  Measured beside it (HIP graphs):
-// us and in parentheses expected, eight weights in turn: 16 x 4096 x 14336 15.6 (14.8), 16 x 14336 x 4096 13.4 (11.7),
-// 32 17.6 (15.3), 64 x 4096 x 14336 27 (28), 128 40 (47); tiled: 256 x 14336 x 4096 58 (55), 2047 x 28672 x 8192 994
-// (1028), where the slab kernel would take 88 and 2400.
+// us and in parentheses expected, eight weights in turn: 16 x 4096 x 14336 14.2 (14.8), 16 x 14336 x 4096 11.9 (11.7),
+// 32 17.3 (15.3), 64 x 4096 x 14336 28 (28), 48 x 14336 x 4096 21 to 23 (24.9), 128 33 to 36 (45.6); tiled: 256 x 14336 x
+// 4096 57 (55), 2047 x 28672 x 8192 961 to 1000 (1028), where the slab kernel takes 65 and 2330.  Slices with 32-token
+// tiles are priced too low and 8 column waves too high: 80 and 96 x 14336 x 4096 are cut in three and take 40 and 42
+// to 47 (38 and 39), where uncut with 8 column waves, expected at 43.6 and 43.9, they take 32 and 33.
 #include <math.h>
 #include <stdio.h>
 #include <stdlib.h>

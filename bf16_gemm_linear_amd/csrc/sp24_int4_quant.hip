@@ -8,8 +8,8 @@
 // fp32 holds them give the codes of exact arithmetic.
 //
 // A lane takes 8 values (a 16-byte load, a 4-byte store), group / 8 lanes a group: one pass, the group's extremes by
-// register exchanges.  HBM bounds both ways: 28672 x 8192 by 64 with zero points (598 MB) 124 to 142 us, back 114 to
-// 120 (5.0 to 5.2 TB/s; a copy 5.17); 4096 x 14336 by 128 26 and 29.
+// register exchanges.  HBM bounds both ways: 28672 x 8192 by 64 with zero points (598 MB) 115 to 143 us, back 113 to
+// 121 (a copy's rate, 5.2 TB/s, gives 116 and 119); 4096 x 14336 by 128 26 and 29.
 #include "sp24_fp8.hpp"
 #include "sp24_int4.hpp"
 #include "sp24_mx4.hpp"

@@ -1,5 +1,6 @@
-// Products with integer 4-bit weights for a few to about a hundred tokens (or an expert's): the weight's
-// bytes are the time, and behind them the bytes of X that every workgroup takes from L2.
+// Products with integer 4-bit weights for 3 tokens to some hundreds (up to 1024 where rows of W are few or long; or
+// an expert's tokens): to about 32 the weight's bytes are the time, and behind them the bytes of X that every
+// workgroup takes from L2, above it W's widening for each tile of tokens.
 //
 // A workgroup owns `cbs` column blocks (of 16 RB rows of W; GATED: 16 gate rows and their up rows), up to
 // 16 MB tokens and a slice of K.  It puts X's slice into LDS once; its waves, cbs of them along the
@@ -17,11 +18,11 @@
 // the workgroup's columns, are taken off behind a group's sum.  Rows past the last are the last one again; their
 // outputs are not stored.
 //
-// 16 x 4096 x 14336 with zero points takes 12.4 to 13.4 us and 2.8 to 3.9 for the join (14.1 a call), 16 x 14336 x
-// 4096 11.6; what is left over the weight's 6 is X, a launch and its end.  77 x 6144 x 4096 by groups of 32
-// takes 20.3, of which about 12 are the vector instructions that widen W for each of five row tiles and scale a
-// sum every 32 values.  Tiles of 48 tokens and more widen less and spill.  64 experts of 4096 x 1792 at 29 tokens:
-// 112 to 117 us gated (492 MB: 4.2 to 4.4 TB/s), 65 to 68 down.
+// 16 x 4096 x 14336 with zero points takes 11.6 to 12.5 us and 2.6 to 3.9 for the join (14.4 a call), 16 x 14336 x
+// 4096 11.9; what is left over the weight's 6 is X, a launch and its end.  77 x 6144 x 4096 by groups of 32
+// takes 21.2 to 22.3, of which about 12 are the vector instructions that widen W for each of five row tiles and scale a
+// sum every 32 values.  Tiles of 48 tokens and more widen less and spill.  64 experts of 4096 x 1792 at 29 tokens,
+// with zero points: 114 to 116 us gated (492 MB: 4.2 to 4.3 TB/s), 65 to 66 down.
 #include "sp24_dma.hpp"
 #include "sp24_int4.hpp"
 #include "sp24_mx4.hpp"

@@ -17,8 +17,8 @@
 // accumulator register 4 g + e is token 8 g + 4 (l / 32) + e, W row l % 32.  LDS rows of 128 bytes are
 // XOR-swizzled in pieces of 16; the swizzle of X is applied on the global side.
 //
-// 2047 x 28672 x 8192 takes 0.98 to 1.06 ms (910 to 980 TFLOP/s; the library's bf16 product of 8192^3, without
-// anything to widen, 1190), its matrix cores busy 42% of the cycles: with 64 KB a step and all registers taken there is
+// 2047 x 28672 x 8192 takes 0.98 to 1.08 ms (890 to 980 TFLOP/s; the library's bf16 product of that size, without
+// anything to widen and with four times the bytes of W, 0.68 to 0.78), its matrix cores busy 42% of the cycles: with 64 KB a step and all registers taken there is
 // one workgroup a CU, whose waves meet at every step.  Tiles of 128 x 128, two workgroups a CU, widen every code
 // twice as often; they win where 256 x 256 would leave CUs idle (the table beside the experts' plan).
 #include <type_traits>

@@ -12,9 +12,9 @@
 // the chunks through LDS, in a fixed order; the experts' down product keeps the slots of a token apart until each
 // is finished, then adds them in their order, times their weights.
 //
-// One token of 14336 x 4096 (30.3 MB) takes 6.7 to 7.6 us (4.0 to 4.5 TB/s; a copy reaches 5.17), a call after
-// another 7.6; two tokens 8.9 in a graph, as many again of the products.  The experts' block of one
-// token, 8 of 64 experts of 4096 x 1792: gated 12.9 to 13.8 us (60 MB: 4.4 to 4.7 TB/s), down 7.6 to 8.5.  8 rows a
+// One token of 14336 x 4096 (30.3 MB) takes 6.8 to 7.1 us (4.3 to 4.5 TB/s; a copy reaches 5.2), a call after
+// another 7.1; two tokens 8.9 in a graph, as many again of the products.  The experts' block of one
+// token, 8 of 64 experts of 4096 x 1792: gated 11.8 to 12.2 us (60 MB: 5 TB/s), down 8.2 to 8.4.  8 rows a
 // workgroup: with 4 each lane's x would be read twice as often; 16 leave fewer waves than fill the CUs.
 #include "sp24_int4.hpp"
 #include "sp24_mx4.hpp"

@@ -573,8 +573,8 @@ size_t sp24_ffn_mxfp4_workspace_size(int64_t m, int64_t d, int64_t f);
  *   zeros_out NULL: s = bf16_rne(amax / 7), q = clamp(rne(w / s), -8, 7) + 8;
  *   else lo = min(0, min w), hi = max(0, max w), s = bf16_rne((hi - lo) / 15),
  *     z = clamp(rne(-lo / s), 0, 15), q = clamp(rne(w / s) + z, 0, 15);
- * s = 1 where that is 0.  fp32 arithmetic, IEEE divisions.  A group with an Inf or a
- * NaN gets s = NaN and q = z = 8.
+ * s = 1 where that is 0.  Codes and scales are those of exact quotients.  A group with an
+ * Inf or a NaN gets s = NaN and q = z = 8.
  *   1 <= rows <= 2^21, group <= cols <= 2^20.  No workspace. */
 int sp24_quant_int4(const void* w_bf16, int64_t rows, int64_t cols, int64_t group, uint8_t* codes_out,
                     void* scales_out_bf16, uint8_t* zeros_out, void* stream);
